@@ -15,6 +15,8 @@ TP_OP_FWD, TP_OP_BWD, TP_OP_DBWD = 0, 1, 2
 TP_LINEAR_TENSOR_CORES, TP_LINEAR_CUDA_CORES = 1, 2
 
 _p = C.c_void_p
+_f32 = C.c_float
+_f64 = C.c_double
 _i64 = C.c_int64
 _i32 = C.c_int32
 _sz = C.c_size_t
@@ -64,6 +66,27 @@ SIGNATURES = {
     "tp_gate_fwd": (C.c_int, [_p, _i64, _p, _p, _p]),
     "tp_gate_bwd": (C.c_int, [_p, _i64, _p, _p, _p, _p]),
     "tp_gate_dbwd": (C.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p]),
+    "tp_norm_create": (C.c_int, [C.POINTER(_p), C.c_char_p, _f64]),
+    "tp_norm_destroy": (C.c_int, [_p]),
+    "tp_norm_query": (C.c_int, [_p, C.POINTER(_i64), C.POINTER(_i64), C.POINTER(_i64)]),
+    "tp_norm_workspace_size": (C.c_int, [_p, _i64, _i32, C.POINTER(_sz)]),
+    "tp_norm_fwd": (C.c_int, [_p, _i64, _p, _p, _p, _p, _p]),
+    "tp_norm_bwd": (C.c_int, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "tp_dropout_create": (C.c_int, [C.POINTER(_p), C.c_char_p]),
+    "tp_dropout_destroy": (C.c_int, [_p]),
+    "tp_dropout_query": (C.c_int, [_p, C.POINTER(_i64), C.POINTER(_i64)]),
+    "tp_dropout_fwd": (C.c_int, [_p, _i64, _p, _f64, _p, _i64, _p, _p]),
+    "tp_dropout_bwd": (C.c_int, [_p, _i64, _p, _f64, _p, _i64, _p, _p]),
+    # neighbour attention and distance buckets (include/tp_attn.h)
+    "tp_attn_create": (C.c_int, [C.POINTER(_p), C.c_char_p, C.c_char_p, _i32, _i32]),
+    "tp_attn_destroy": (C.c_int, [_p]),
+    "tp_attn_query": (C.c_int, [_p, C.POINTER(_i64), C.POINTER(_i64)]),
+    "tp_attn_workspace_size": (C.c_int, [_p, _i64, _i64, _i32, C.POINTER(_sz)]),
+    "tp_attn_fwd": (C.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _f32, _f64, _p, _i64,
+                              _p, _p, _p, _sz, _p]),
+    "tp_attn_bwd": (C.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _f32, _f64, _p,
+                              _i64, _p, _p, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _sz, _p]),
+    "tp_distance_buckets": (C.c_int, [_i64, _p, _i32, _p, _f32, _p, _p]),
 }
 
 _LIB = None

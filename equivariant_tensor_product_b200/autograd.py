@@ -3,6 +3,7 @@ own backward -> tp_conv_dbwd, so force training (a loss on d(energy)/d(positions
 differentiate twice through the convolution (uvu; uvw mode differentiates once, to x, the
 edge vectors, the per-edge scalars and the shared mixing weights W; the radial-projection form
 differentiates once, to x, the edge vectors, the hidden layer h and the output matrix W_r).
+Attention and norm differentiate once; dropout, linear in x, any number of times.
 Marshalling only (see ops.py)."""
 from __future__ import annotations
 
@@ -203,3 +204,95 @@ def tp_conv_radial(plan: Plan, graph: Graph, x, vec, h, Wr):
     if plan.mode == TP_MODE_UVW:
         raise ValueError("the fused radial projection is implemented for uvu plans")
     return TPConvRadial.apply(x, vec, h, Wr, plan, graph)
+
+
+# ---------------------------------------------------------------------------------------------
+# Graph attention (include/tp_attn.h), norm and dropout (include/tp_block.h)
+# ---------------------------------------------------------------------------------------------
+
+from .attn import Attention, tp_attn_bwd, tp_attn_fwd  # noqa: E402
+from .block import Dropout, Norm, tp_dropout_bwd, tp_norm_bwd, tp_norm_fwd  # noqa: E402
+
+
+def _row_strided(t):
+    """t itself when the library can read its rows in place (a column slice), else a copy."""
+    ok = t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1])
+    return t if ok else t.contiguous()
+
+
+class AttnFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, table, bucket, rng, attn, graph, scale, p, site):
+        q, k, v = _row_strided(q), _row_strided(k), _row_strided(v)
+        table = None if table is None else table.contiguous()
+        y, lse = tp_attn_fwd(attn, graph.rowptr, graph.src, q, k, v, bucket=bucket, table=table, scale=scale, p=p,
+                             rng=rng, site=site)
+        ctx.save_for_backward(q, k, v, table, bucket, rng, y, lse)
+        ctx.attn, ctx.graph, ctx.rest = attn, graph, (scale, p, site)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        q, k, v, table, bucket, rng, y, lse = ctx.saved_tensors
+        scale, p, site = ctx.rest
+        n = ctx.needs_input_grad
+        colptr, perm = ctx.graph.transpose() if n[1] or n[2] else (None, None)
+        gq, gk, gv, gtable = tp_attn_bwd(ctx.attn, ctx.graph.rowptr, ctx.graph.src, q, k, v, y, lse, gy.contiguous(),
+                                         bucket=bucket, table=table, scale=scale, p=p, rng=rng, site=site,
+                                         colptr=colptr, perm=perm, need_gq=n[0], need_gk=n[1], need_gv=n[2],
+                                         need_gtable=n[3])
+        return gq, gk, gv, gtable, None, None, None, None, None, None, None
+
+
+def tp_attn(attn: Attention, graph: Graph, q, k, v, bucket=None, table=None, scale=None, p: float = 0.0, rng=None,
+            site: int = 0):
+    """y = attention(q, k, v) over the graph's edges with first-order derivatives to q, k, v and table through
+    the CUDA kernels.  q, k, v may be column slices of one array.  rng must not change between the forward
+    and the backward call (autograd reports it when it does)."""
+    return AttnFn.apply(q, k, v, table, bucket, rng if p > 0.0 else None, attn, graph, scale, p, site)
+
+
+class NormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, norm):
+        x = x.contiguous()
+        weight = None if weight is None else weight.contiguous()
+        y = tp_norm_fwd(norm, x, weight, None if bias is None else bias.contiguous())
+        ctx.save_for_backward(x, weight)
+        ctx.norm = norm
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, weight = ctx.saved_tensors
+        n = ctx.needs_input_grad
+        gx, gw, gb = tp_norm_bwd(ctx.norm, x, gy.contiguous(), weight, need_gx=n[0], need_gweight=n[1],
+                                 need_gbias=n[2])
+        return gx, gw, gb, None
+
+
+def tp_norm(norm: Norm, x, weight=None, bias=None):
+    """y = norm(x) with first-order derivatives to x, weight and bias through the CUDA kernels."""
+    return NormFn.apply(x, weight, bias, norm)
+
+
+class DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rng, drop, p, site):
+        ctx.save_for_backward(rng)
+        ctx.drop, ctx.rest = drop, (p, site)
+        # the forward and backward calls are one linear map and its adjoint, which is the map itself
+        return tp_dropout_bwd(drop, x.contiguous(), p, rng, site)
+
+    @staticmethod
+    def backward(ctx, gy):
+        (rng,) = ctx.saved_tensors
+        return DropoutFn.apply(gy, rng, ctx.drop, *ctx.rest), None, None, None, None
+
+
+def tp_dropout(drop: Dropout, x, p: float, rng=None, site: int = 0):
+    """y = x with whole channels dropped, differentiable any number of times.  rng must not change between the
+    forward and the backward call (autograd reports it when it does)."""
+    return DropoutFn.apply(x, rng if p > 0.0 else None, drop, p, site)

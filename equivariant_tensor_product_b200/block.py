@@ -1,5 +1,5 @@
-"""Python binding of the node-side operators (include/tp_block.h): the irreps-wise linear map
-and the gate.  Same names as the C ABI, argument marshalling only: every step runs in
+"""Python binding of the node-side operators (include/tp_block.h): the irreps-wise linear map,
+the gate, the norm and the dropout.  Same names as the C ABI, argument marshalling only: every step runs in
 libtp.so, on the current torch stream."""
 from __future__ import annotations
 
@@ -9,10 +9,12 @@ from typing import Optional, Sequence
 import torch
 
 from ._lib import TP_OP_BWD, TP_OP_FWD, check, load
+from .attn import _on, _same_device, _shape, _workspace
 from .ops import _ptr, _stream
 
 __all__ = ["Linear", "Gate", "tp_linear_fwd", "tp_linear_bwd", "tp_linear_workspace_size", "tp_gate_fwd",
-           "tp_gate_bwd", "tp_gate_dbwd"]
+           "tp_gate_bwd", "tp_gate_dbwd", "Norm", "Dropout", "tp_norm_fwd", "tp_norm_bwd", "tp_norm_workspace_size",
+           "tp_dropout_fwd", "tp_dropout_bwd"]
 
 
 class Linear:
@@ -129,3 +131,119 @@ def tp_gate_dbwd(gate: Gate, x, gy, ggx, need_g_gy=True, need_g_x=True, stream=N
                               _ptr(ggx, torch.float32, "ggx"), _ptr(g_gy, torch.float32, "g_gy"),
                               _ptr(g_x, torch.float32, "g_x"), _stream(stream)), "tp_gate_dbwd")
     return g_gy, g_x
+
+
+class Norm:
+    """Owns a tp_norm_t: layer normalisation of irreps rows, block by block (0e blocks lose their mean over
+    channels and have a bias, every other block is only scaled)."""
+
+    def __init__(self, irreps: str, eps: float = 1e-5):
+        lib = load()
+        self._lib = lib
+        self.handle = C.c_void_p()
+        self.irreps, self.eps = irreps, float(eps)
+        check(lib.tp_norm_create(C.byref(self.handle), irreps.encode(), self.eps), "tp_norm_create")
+        vals = [C.c_int64() for _ in range(3)]
+        check(lib.tp_norm_query(self.handle, *[C.byref(v) for v in vals]), "tp_norm_query")
+        self.dim, self.n_weights, self.n_bias = (v.value for v in vals)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value:
+            self._lib.tp_norm_destroy(h)
+            self.handle = None
+
+
+def tp_norm_workspace_size(norm: Norm, N: int, op: int) -> int:
+    out = C.c_size_t()
+    check(load().tp_norm_workspace_size(norm.handle, int(N), int(op), C.byref(out)), "tp_norm_workspace_size")
+    return out.value
+
+
+def _norm_inputs(norm, x, weight, bias):
+    N, dev = x.shape[0], x.device
+    _shape(x, (N, norm.dim), "x")
+    _shape(weight, (norm.n_weights,), "weight")
+    _shape(bias, (norm.n_bias,), "bias")
+    _same_device(dev, weight=weight, bias=bias)
+    return N, dev
+
+
+def tp_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, stream=None):
+    """y = norm(x); weight [n_weights] and bias [n_bias] default to ones and zeros.  y may be x."""
+    N, dev = _norm_inputs(norm, x, weight, bias)
+    _shape(y, (N, norm.dim), "y")
+    _same_device(dev, y=y)
+    with _on(dev, stream):
+        y = torch.empty(N, norm.dim, dtype=torch.float32, device=dev) if y is None else y
+        check(load().tp_norm_fwd(norm.handle, N, _ptr(x, torch.float32, "x"), _ptr(weight, torch.float32, "weight"),
+                                 _ptr(bias, torch.float32, "bias"), _ptr(y, torch.float32, "y"),
+                                 torch.cuda.current_stream(dev).cuda_stream), "tp_norm_fwd")
+    return y
+
+
+def tp_norm_bwd(norm: Norm, x, gy, weight=None, need_gx=True, need_gweight=True, need_gbias=True, gx=None,
+                gweight=None, gbias=None, ws=None, stream=None):
+    """(gx, gweight, gbias) against gy, each None when not requested.  gx may be gy."""
+    N, dev = _norm_inputs(norm, x, weight, None)
+    _same_device(dev, gy=gy, gx=gx, gweight=gweight, gbias=gbias, ws=ws)
+    for t, shape, name in ((gy, (N, norm.dim), "gy"), (gx, (N, norm.dim), "gx"),
+                           (gweight, (norm.n_weights,), "gweight"), (gbias, (norm.n_bias,), "gbias")):
+        _shape(t, shape, name)
+    with _on(dev, stream):
+        new = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=dev)
+        gx = new(N, norm.dim) if gx is None and need_gx else gx
+        gweight = new(norm.n_weights) if gweight is None and need_gweight else gweight
+        gbias = new(norm.n_bias) if gbias is None and need_gbias else gbias
+        ws = _workspace(ws, tp_norm_workspace_size(norm, N, TP_OP_BWD), dev)
+        check(load().tp_norm_bwd(norm.handle, N, _ptr(x, torch.float32, "x"), _ptr(weight, torch.float32, "weight"),
+                                 _ptr(gy, torch.float32, "gy"), _ptr(gx, torch.float32, "gx"),
+                                 _ptr(gweight, torch.float32, "gweight"), _ptr(gbias, torch.float32, "gbias"),
+                                 ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 torch.cuda.current_stream(dev).cuda_stream), "tp_norm_bwd")
+    return gx, gweight, gbias
+
+
+class Dropout:
+    """Owns a tp_dropout_t: dropout of whole channels of irreps rows."""
+
+    def __init__(self, irreps: str):
+        lib = load()
+        self._lib = lib
+        self.handle = C.c_void_p()
+        self.irreps = irreps
+        check(lib.tp_dropout_create(C.byref(self.handle), irreps.encode()), "tp_dropout_create")
+        a, b = C.c_int64(), C.c_int64()
+        check(lib.tp_dropout_query(self.handle, C.byref(a), C.byref(b)), "tp_dropout_query")
+        self.dim, self.n_channels = a.value, b.value
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value:
+            self._lib.tp_dropout_destroy(h)
+            self.handle = None
+
+
+def _dropout(name, drop, x, p, rng, site, y, stream):
+    N, dev = x.shape[0], x.device
+    _shape(x, (N, drop.dim), "input")
+    _shape(y, (N, drop.dim), "output")
+    _shape(rng, (2,), "rng")
+    _same_device(dev, rng=rng, output=y)
+    with _on(dev, stream):
+        y = torch.empty(N, drop.dim, dtype=torch.float32, device=dev) if y is None else y
+        check(getattr(load(), name)(drop.handle, N, _ptr(x, torch.float32, "input"), float(p),
+                                    _ptr(rng, torch.int64, "rng"), int(site), _ptr(y, torch.float32, "output"),
+                                    torch.cuda.current_stream(dev).cuda_stream), name)
+    return y
+
+
+def tp_dropout_fwd(drop: Dropout, x, p: float, rng=None, site: int = 0, y=None, stream=None):
+    """y = x with whole channels dropped with probability p and the rest scaled by 1/(1-p); rng is an int64
+    CUDA tensor (seed, offset), site tells the calls of one step apart.  y may be x."""
+    return _dropout("tp_dropout_fwd", drop, x, p, rng, site, y, stream)
+
+
+def tp_dropout_bwd(drop: Dropout, gy, p: float, rng=None, site: int = 0, gx=None, stream=None):
+    """gx: the choice of tp_dropout_fwd with the same p, rng and site, drawn again, applied to gy."""
+    return _dropout("tp_dropout_bwd", drop, gy, p, rng, site, gx, stream)

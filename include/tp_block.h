@@ -38,6 +38,23 @@
  * channels of the gated blocks counted in order) is multiplied by sigmoid(gate channel c).
  * Gates must be 0e and their total multiplicity must equal that of the gated blocks.
  *
+ * Norm.  Layer normalisation of a row, block by block: with c channels of width d = 2l+1,
+ * mu = the mean over channels for 0e blocks and 0 for all others, rho = (mean over the block's
+ * c d floats of (x - mu)^2 + eps)^(-1/2) and n = (x - mu) rho,
+ *
+ *   y[u, m] = n[u, m] weight[u] (+ bias[u] in 0e blocks).
+ *
+ * 0e blocks get the ordinary layer norm; every other block is scaled by invariants, which
+ * keeps its directions and parity (a mean over channels of l > 0 or odd blocks is subtracted
+ * nowhere).  weight has one entry per channel in row order, bias one per 0e channel.
+ * Backward, with g = gy weight: gx = rho (g - [0e] mean g - n mean(g n)), gweight[u] = sum over
+ * rows and m of gy n, gbias[u] = sum over rows of gy; statistics are formed again from x.
+ *
+ * Dropout.  y[n, u, m] = x[n, u, m] r[n, u], r = 0 or 1/(1-p): one choice per channel, shared by
+ * its components m, so that the rows stay equivariant.  r[n, u] is value number n C + u (C
+ * channels a row, in row order) of the generator described in tp_attn.h, never stored; the
+ * backward pass is the same call on gy.
+ *
  * Layouts as in tp.h: [N, dim] row-major fp32 device arrays, blocks in irreps order, [u][m]
  * inside a block.  Ownership: the caller owns every buffer (workspace included); the
  * library owns the linear and gate handles (host memory).  Streams: every call enqueues on
@@ -108,6 +125,42 @@ tp_status_t tp_gate_bwd(tp_gate_t gate, int64_t N, const float* x, const float* 
  * g_x[N, in_dim] = the second-derivative terms; each NULL output is skipped. */
 tp_status_t tp_gate_dbwd(tp_gate_t gate, int64_t N, const float* x, const float* gy, const float* ggx,
                          float* g_gy, float* g_x, tp_stream_t stream);
+
+typedef struct tp_norm_s* tp_norm_t;
+typedef struct tp_dropout_s* tp_dropout_t;
+
+/* Builds a norm of rows of `irreps` (l <= 3, at most 16 blocks, rows of at most 8,192 floats);
+ * eps > 0 and finite. */
+tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps);
+tp_status_t tp_norm_destroy(tp_norm_t norm);
+/* Row width, entries of weight (channels) and of bias (0e channels). */
+tp_status_t tp_norm_query(tp_norm_t norm, int64_t* dim, int64_t* n_weights, int64_t* n_bias);
+
+/* Device workspace bytes for N rows: TP_OP_FWD 0; TP_OP_BWD the per-CTA partials of the weight
+ * gradients (a few hundred rows). */
+tp_status_t tp_norm_workspace_size(tp_norm_t norm, int64_t N, int32_t op, size_t* bytes);
+
+/* y[N, dim] = norm(x[N, dim]); weight NULL = ones, bias NULL = zeros.  y may be x. */
+tp_status_t tp_norm_fwd(tp_norm_t norm, int64_t N, const float* x, const float* weight, const float* bias, float* y,
+                        tp_stream_t stream);
+
+/* Against gy[N, dim]: gx[N, dim], gweight[n_weights], gbias[n_bias]; each NULL output is
+ * skipped.  N = 0 zeroes gweight and gbias.  gx may be gy.  Sums over rows run in a fixed order. */
+tp_status_t tp_norm_bwd(tp_norm_t norm, int64_t N, const float* x, const float* weight, const float* gy, float* gx,
+                        float* gweight, float* gbias, void* ws, size_t ws_bytes, tp_stream_t stream);
+
+/* Builds a dropout of rows of `irreps` (l <= 3, at most 16 blocks, rows of at most 8,192 floats). */
+tp_status_t tp_dropout_create(tp_dropout_t* drop, const char* irreps);
+tp_status_t tp_dropout_destroy(tp_dropout_t drop);
+tp_status_t tp_dropout_query(tp_dropout_t drop, int64_t* dim, int64_t* n_channels);
+
+/* y[N, dim] = dropout(x[N, dim]) with probability p in [0, 1); rng = {seed, offset} in device
+ * memory and site as in tp_attn.h.  A dropped channel is 0 whatever x holds there.  y may be x. */
+tp_status_t tp_dropout_fwd(tp_dropout_t drop, int64_t N, const float* x, double p, const int64_t* rng, int64_t site,
+                           float* y, tp_stream_t stream);
+/* gx = the same choice applied to gy. */
+tp_status_t tp_dropout_bwd(tp_dropout_t drop, int64_t N, const float* gy, double p, const int64_t* rng, int64_t site,
+                           float* gx, tp_stream_t stream);
 
 #ifdef __cplusplus
 }
