@@ -11,6 +11,13 @@
 // buckets of 32 edges are read by the 32 lanes, edges that take no part are struck out by a
 // ballot, and the rest goes U edges at a time, with all 2 U row gathers issued before the first
 // use.  The softmax runs in one pass with the running maximum and sum.
+//
+// Long rows.  A receiver (sender) of more than `hub` edges would keep one warp busy long after the
+// others are done.  Its edges are taken window by window instead: the edge axis is cut into
+// windows of win = hub / 2 edges, one CTA each, behind the CTAs of the rows.  A window meets at
+// most two such rows (the row of its first edge and the row of its last one), finds them by a
+// 33-way search in the row pointers and leaves a partial row for each; k_attn_join adds a row's
+// partials up in window order.  Graphs of at most `hub` edges have neither windows nor the join.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -42,6 +49,10 @@ struct AttnArgs {
   int N, E, H, K;
   int hw, groups;            // heads per warp (a power of two), head groups of a row
   int W;                     // warps that split a row's edges
+  int row_ctas;              // CTAs of the rows; the windows' CTAs come after them
+  int hub, win, n_win;       // rows of more than hub edges go by windows (n_win = 0: no such rows)
+  float* part;               // workspace [n_win][2][part_len]: partial rows of the windows
+  int part_len;
   int dq, dv;
   const int32_t* rowptr;
   const int32_t* src;
@@ -71,6 +82,8 @@ struct AttnArgs {
   int hist_ctas, hist_copies, hist_lanes;
   HeadMap mq, mv;
 };
+
+constexpr int kMinWindow = 128;
 
 __device__ __forceinline__ int slot_offset(const HeadMap& m, int h, int pos) {
   for (int b = 0; b < m.nb; ++b) {
@@ -112,35 +125,123 @@ __device__ __forceinline__ void store_vec(float* p, const Vec<V>& r) {
 
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
 
-// What a thread works on: its receiver (or sender), head and chunks.
+__device__ __forceinline__ int clamp_edge(int e, int E) { return min(max(e, 0), E); }
+
+// The row r of `ptr` with ptr[r] <= e < ptr[r + 1], or -1: 32 probes a step, the same answer in every lane.
+__device__ __forceinline__ int find_row(const int32_t* __restrict__ ptr, int N, int e) {
+  if (e < __ldg(ptr) || e >= __ldg(ptr + N)) return -1;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 32) / 33;
+    const int64_t pos = lo + (int64_t)(lane + 1) * step;
+    const int below = __popc(__ballot_sync(kFull, pos < hi && __ldg(ptr + min(pos, (int64_t)hi)) <= e));
+    lo += below * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// A stretch of one row's edges that a CTA's warps work on: a whole row, or a window's share of a long one.
+struct Task {
+  int row, head0, split, W, lo, hi;
+  float* part;               // where a window leaves its partial row
+  bool write;                // false: a long row, which the windows deal with
+};
+
+// Number of tasks of this CTA.  Rows: one.  Windows: the heads of up to two rows, found here.
+struct Tasks {
+  int n, first, row0, row1;
+
+  __device__ __forceinline__ Tasks(const AttnArgs& a, const int32_t* __restrict__ ptr, bool wide) {
+    __shared__ int found[2];
+    n = 1;
+    if ((int)blockIdx.x < a.row_ctas) return;
+    first = ((int)blockIdx.x - a.row_ctas) * a.win;
+    if (threadIdx.x < 64) {
+      const int slot = threadIdx.x >> 5;
+      int r = find_row(ptr, a.N, slot ? min(first + a.win, a.E) - 1 : first);
+      if (r >= 0) {
+        const int start = __ldg(ptr + r);
+        if (__ldg(ptr + r + 1) - start <= a.hub || (slot && start <= first)) r = -1;
+      }
+      if ((threadIdx.x & 31) == 0) found[slot] = r;
+    }
+    __syncthreads();
+    row0 = found[0];
+    row1 = found[1];
+    n = 2 * (wide ? a.H : a.groups);
+  }
+
+  __device__ __forceinline__ Task get(const AttnArgs& a, const int32_t* __restrict__ ptr, int i, bool wide) const {
+    Task t;
+    const int warp = threadIdx.x >> 5;
+    t.part = nullptr;
+    t.write = false;
+    t.row = a.N;
+    t.lo = t.hi = t.head0 = t.split = 0;
+    t.W = 1;
+    if ((int)blockIdx.x < a.row_ctas) {
+      if (wide) {
+        t.row = blockIdx.x / a.H;
+        t.head0 = blockIdx.x - t.row * a.H;
+      } else {
+        const int unit = blockIdx.x * (kAttnWarps / a.W) + warp / a.W;
+        t.W = a.W;
+        t.split = warp % a.W;
+        t.row = unit / a.groups;
+        t.head0 = (unit - t.row * a.groups) * a.hw;
+      }
+      if (t.row >= a.N) return t;
+      t.lo = clamp_edge(__ldg(ptr + t.row), a.E);
+      t.hi = clamp_edge(__ldg(ptr + t.row + 1), a.E);
+      t.write = a.n_win == 0 || t.hi - t.lo <= a.hub;
+      if (!t.write) t.hi = t.lo;
+    } else {
+      const int per = wide ? a.H : a.groups, slot = i / per;
+      const int r = slot ? row1 : row0;
+      if (r < 0) return t;
+      t.row = r;
+      t.head0 = (i - slot * per) * (wide ? 1 : a.hw);
+      t.write = true;
+      t.part = a.part + ((int64_t)((int)blockIdx.x - a.row_ctas) * 2 + slot) * a.part_len;
+      t.lo = max(__ldg(ptr + t.row), first);
+      t.hi = min(min(__ldg(ptr + t.row + 1), first + a.win), a.E);
+      if (!wide) {
+        t.W = kAttnWarps;
+        t.split = warp;
+      }
+    }
+    if (t.W > 1 && t.hi > t.lo) {
+      const int per = (t.hi - t.lo + t.W - 1) / t.W;
+      t.lo += min(t.split * per, t.hi - t.lo);
+      t.hi = min(t.hi, t.lo + per);
+    }
+    return t;
+  }
+};
+
+// Which head and chunks of the task's row a thread holds.
 template <int V, int S, bool WIDE>
 struct Lane {
-  int row, h, head0, G, gl, split, sub;
+  int h, G, gl, sub;
   bool live;                 // the lane holds a head of a row
   int oq[S], ov[S];
 
-  __device__ __forceinline__ explicit Lane(const AttnArgs& a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __device__ __forceinline__ Lane(const AttnArgs& a, const Task& t) {
+    const int lane = threadIdx.x & 31;
     if constexpr (WIDE) {
-      row = blockIdx.x / a.H;
-      h = blockIdx.x - row * a.H;
-      head0 = h;
+      h = t.head0;
       sub = 0;
       G = blockDim.x;
       gl = threadIdx.x;
-      split = 0;
-      live = true;
     } else {
-      const int unit = blockIdx.x * (kAttnWarps / a.W) + warp / a.W;
-      split = warp % a.W;
-      row = unit / a.groups;
-      head0 = (unit - row * a.groups) * a.hw;
       G = 32 / a.hw;
       sub = lane / G;
       gl = lane & (G - 1);
-      h = head0 + sub;
-      live = row < a.N && h < a.H;
+      h = t.head0 + sub;
     }
+    live = t.write && t.row < a.N && h < a.H;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
       const int pos = (s * G + gl) * V;
@@ -175,8 +276,6 @@ struct Lane {
     }
   }
 };
-
-__device__ __forceinline__ int clamp_edge(int e, int E) { return min(max(e, 0), E); }
 
 // One lane's edge of a batch of 32: sender (-1: takes no part), bucket, and a bit per head of the warp
 // that is set where dropout keeps the probability.
@@ -213,31 +312,24 @@ __device__ __forceinline__ EdgeLane read_edge(const AttnArgs& a, const DropKey& 
 template <int V, int S, int U, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_fwd(const __grid_constant__ AttnArgs a) {
   __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * S + 2) * 32];
-  const Lane<V, S, WIDE> L(a);
   const int lane = threadIdx.x & 31;
   int turn = 0;
+  DropKey key{};
+  if (a.drop.rng) key = drop_key(a.drop);
+  const Tasks tasks(a, a.rowptr, WIDE);
+  for (int task = 0; task < tasks.n; ++task) {
+  const Task t = tasks.get(a, a.rowptr, task, WIDE);
+  const Lane<V, S, WIDE> L(a, t);
   Vec<V> q[S], acc[S];
   float m = -INFINITY, l = 0.0f;
-  int lo = 0, hi = 0;
-  if (L.row < a.N) {
-    lo = clamp_edge(__ldg(a.rowptr + L.row), a.E);
-    hi = clamp_edge(__ldg(a.rowptr + L.row + 1), a.E);
-    if (!WIDE && a.W > 1 && hi > lo) {
-      const int per = (hi - lo + a.W - 1) / a.W;
-      lo += min(L.split * per, hi - lo);
-      hi = min(hi, lo + per);
-    }
-  }
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    q[s] = load_vec<V>(a.q + (int64_t)L.row * a.ldq + L.oq[s], L.oq[s] >= 0);
+    q[s] = load_vec<V>(a.q + (int64_t)t.row * a.ldq + L.oq[s], L.oq[s] >= 0);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[s].x[i] = 0.0f;
   }
-  DropKey key{};
-  if (a.drop.rng) key = drop_key(a.drop);
-  for (int base = lo; base < hi; base += 32) {
-    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < hi, L.head0, WIDE ? 1 : a.hw);
+  for (int base = t.lo; base < t.hi; base += 32) {
+    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, WIDE ? 1 : a.hw);
     uint32_t left = __ballot_sync(kFull, mine.j >= 0);
     while (left) {
       Vec<V> kk[U][S], vv[U][S];
@@ -245,12 +337,12 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
       bool kept[U], on[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = left ? __ffs(left) - 1 : 0;
+        const int at = left ? __ffs(left) - 1 : 0;
         on[u] = left != 0;
         left &= left - 1;
-        const int64_t j = __shfl_sync(kFull, mine.j, t);
-        const int b = __shfl_sync(kFull, mine.b, t);
-        kept[u] = (__shfl_sync(kFull, mine.keep, t) >> L.sub) & 1u;
+        const int64_t j = __shfl_sync(kFull, mine.j, at);
+        const int b = __shfl_sync(kFull, mine.b, at);
+        kept[u] = (__shfl_sync(kFull, mine.keep, at) >> L.sub) & 1u;
 #pragma unroll
         for (int s = 0; s < S; ++s) kk[u][s] = load_vec<V>(a.k + j * a.ldk + L.oq[s], on[u] && L.oq[s] >= 0);
 #pragma unroll
@@ -301,10 +393,10 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
     }
   }
   if constexpr (!WIDE) {
-    if (a.W > 1) {                       // join the warps of a row in order
+    if (t.W > 1) {                       // join the warps of a row in order
       const int warp = threadIdx.x >> 5;
       float* mine = join + warp * (V * S + 2) * 32;
-      if (L.split > 0) {
+      if (t.split > 0) {
         mine[lane] = m;
         mine[32 + lane] = l;
 #pragma unroll
@@ -313,8 +405,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
           for (int i = 0; i < V; ++i) mine[(2 + s * V + i) * 32 + lane] = acc[s].x[i];
       }
       __syncthreads();
-      if (L.split > 0) return;
-      for (int w = 1; w < a.W; ++w) {
+      for (int w = 1; t.split == 0 && w < t.W; ++w) {
         const float* other = join + (warp + w) * (V * S + 2) * 32;
         const float m2 = other[lane], top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
         const float f1 = exp_of(m - ref), f2 = exp_of(m2 - ref);
@@ -327,17 +418,30 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
       }
     }
   }
-  if (!L.live) return;
-  const bool none = m == -INFINITY && l == 0.0f;
-  const float f = none ? 0.0f : a.drop.inv_keep / l;
+  if (L.live && t.split == 0) {
+    if (t.part) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (L.ov[s] < 0) continue;
+      for (int s = 0; s < S; ++s)
+        if (L.ov[s] >= 0) store_vec<V>(t.part + L.ov[s], acc[s]);
+      if (L.gl == 0) {
+        t.part[a.part_len - 2 * a.H + L.h] = m;
+        t.part[a.part_len - a.H + L.h] = l;
+      }
+    } else {
+      const bool none = m == -INFINITY && l == 0.0f;
+      const float f = none ? 0.0f : a.drop.inv_keep / l;
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[s].x[i] *= f;
-    store_vec<V>(a.y + (int64_t)L.row * a.dv + L.ov[s], acc[s]);
+      for (int s = 0; s < S; ++s) {
+        if (L.ov[s] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[s].x[i] *= f;
+        store_vec<V>(a.y + (int64_t)t.row * a.dv + L.ov[s], acc[s]);
+      }
+      if (a.lse && L.gl == 0) a.lse[(int64_t)t.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
+    }
   }
-  if (a.lse && L.gl == 0) a.lse[(int64_t)L.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
+  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
+  }
 }
 
 // Backward, receiver order: gq, and for the sender pass and gtable (ds, r p) of every edge and head
@@ -345,28 +449,23 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 template <int V, int S, int U, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_recv(const __grid_constant__ AttnArgs a) {
   __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * 2 * U : kAttnWarps * V * S * 32];
-  const Lane<V, S, WIDE> L(a);
   const int lane = threadIdx.x & 31;
   int turn = 0;
+  DropKey key{};
+  if (a.drop.rng) key = drop_key(a.drop);
+  const Tasks tasks(a, a.rowptr, WIDE);
+  for (int task = 0; task < tasks.n; ++task) {
+  const Task t = tasks.get(a, a.rowptr, task, WIDE);
+  const Lane<V, S, WIDE> L(a, t);
   Vec<V> q[S], gy[S], acc[S];
-  int lo = 0, hi = 0;
-  if (L.row < a.N) {
-    lo = clamp_edge(__ldg(a.rowptr + L.row), a.E);
-    hi = clamp_edge(__ldg(a.rowptr + L.row + 1), a.E);
-    if (!WIDE && a.W > 1 && hi > lo) {
-      const int per = (hi - lo + a.W - 1) / a.W;
-      lo += min(L.split * per, hi - lo);
-      hi = min(hi, lo + per);
-    }
-  }
   float delta[2 * U];
 #pragma unroll
   for (int u = 0; u < 2 * U; ++u) delta[u] = 0.0f;
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    q[s] = load_vec<V>(a.q + (int64_t)L.row * a.ldq + L.oq[s], L.oq[s] >= 0);
-    gy[s] = load_vec<V>(a.gy + (int64_t)L.row * a.dv + L.ov[s], L.ov[s] >= 0);
-    const Vec<V> y = load_vec<V>(a.y_in + (int64_t)L.row * a.dv + L.ov[s], L.ov[s] >= 0);
+    q[s] = load_vec<V>(a.q + (int64_t)t.row * a.ldq + L.oq[s], L.oq[s] >= 0);
+    gy[s] = load_vec<V>(a.gy + (int64_t)t.row * a.dv + L.ov[s], L.ov[s] >= 0);
+    const Vec<V> y = load_vec<V>(a.y_in + (int64_t)t.row * a.dv + L.ov[s], L.ov[s] >= 0);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       acc[s].x[i] = 0.0f;
@@ -375,15 +474,13 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   }
   L.sum(delta, join, turn);
   const float del = delta[0];
-  const float lse = L.live ? __ldg(a.lse_in + (int64_t)L.row * a.H + L.h) : 0.0f;
-  DropKey key{};
-  if (a.drop.rng) key = drop_key(a.drop);
-  for (int base = lo; base < hi; base += 32) {
-    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < hi, L.head0, WIDE ? 1 : a.hw);
-    if (a.rec && base + lane < hi && L.head0 == 0 && (!WIDE || threadIdx.x < 32))
-      a.dst[base + lane] = mine.j >= 0 ? L.row : -1;
-    if (a.rec && base + lane < hi && mine.j < 0 && (!WIDE || threadIdx.x < 32))
-      for (int h = L.head0; h < min(a.H, L.head0 + (WIDE ? 1 : a.hw)); ++h)
+  const float lse = L.live ? __ldg(a.lse_in + (int64_t)t.row * a.H + L.h) : 0.0f;
+  for (int base = t.lo; base < t.hi; base += 32) {
+    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, WIDE ? 1 : a.hw);
+    if (a.rec && base + lane < t.hi && t.head0 == 0 && (!WIDE || threadIdx.x < 32))
+      a.dst[base + lane] = mine.j >= 0 ? t.row : -1;
+    if (a.rec && base + lane < t.hi && mine.j < 0 && (!WIDE || threadIdx.x < 32))
+      for (int h = t.head0; h < min(a.H, t.head0 + (WIDE ? 1 : a.hw)); ++h)
         a.rec[(int64_t)(base + lane) * a.H + h] = make_float2(0.0f, 0.0f);
     uint32_t left = __ballot_sync(kFull, mine.j >= 0);
     while (left) {
@@ -440,30 +537,36 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
     }
   }
   if constexpr (!WIDE) {
-    if (a.W > 1) {
+    if (t.W > 1) {
       const int warp = threadIdx.x >> 5;
-      if (L.split > 0) {
+      if (t.split > 0) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int i = 0; i < V; ++i) join[(warp * S * V + s * V + i) * 32 + lane] = acc[s].x[i];
       }
       __syncthreads();
-      if (L.split > 0) return;
-      for (int w = 1; w < a.W; ++w)
+      for (int w = 1; t.split == 0 && w < t.W; ++w)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
           for (int i = 0; i < V; ++i) acc[s].x[i] += join[((warp + w) * S * V + s * V + i) * 32 + lane];
     }
   }
-  if (!L.live || !a.gq) return;
+  if (L.live && t.split == 0 && a.gq) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (L.oq[s] < 0) continue;
+    for (int s = 0; s < S; ++s) {
+      if (L.oq[s] < 0) continue;
+      if (t.part) {
+        store_vec<V>(t.part + L.oq[s], acc[s]);
+        continue;
+      }
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[s].x[i] *= a.scale;
-    store_vec<V>(a.gq + (int64_t)L.row * a.ldgq + L.oq[s], acc[s]);
+      for (int i = 0; i < V; ++i) acc[s].x[i] *= a.scale;
+      store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + L.oq[s], acc[s]);
+    }
+  }
+  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
@@ -471,29 +574,22 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 template <int V, int S, int U, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_send(const __grid_constant__ AttnArgs a) {
   __shared__ float join[WIDE ? 1 : kAttnWarps * 2 * V * S * 32];
-  const Lane<V, S, WIDE> L(a);
   const int lane = threadIdx.x & 31;
+  const int e_lo = max(__ldg(a.rowptr), 0), e_hi = min(__ldg(a.rowptr + a.N), a.E);
+  const Tasks tasks(a, a.colptr, WIDE);
+  for (int task = 0; task < tasks.n; ++task) {
+  const Task t = tasks.get(a, a.colptr, task, WIDE);
+  const Lane<V, S, WIDE> L(a, t);
   Vec<V> ak[S], av[S];
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int i = 0; i < V; ++i) ak[s].x[i] = av[s].x[i] = 0.0f;
-  int lo = 0, hi = 0;
-  if (L.row < a.N) {
-    lo = clamp_edge(__ldg(a.colptr + L.row), a.E);
-    hi = clamp_edge(__ldg(a.colptr + L.row + 1), a.E);
-    if (!WIDE && a.W > 1 && hi > lo) {
-      const int per = (hi - lo + a.W - 1) / a.W;
-      lo += min(L.split * per, hi - lo);
-      hi = min(hi, lo + per);
-    }
-  }
-  const int e_lo = __ldg(a.rowptr), e_hi = min(__ldg(a.rowptr + a.N), a.E);
-  for (int base = lo; base < hi; base += 32) {
+  for (int base = t.lo; base < t.hi; base += 32) {
     int e = -1, i = -1;
-    if (base + lane < hi) {
+    if (base + lane < t.hi) {
       e = __ldg(a.perm + base + lane);
-      if (e >= max(e_lo, 0) && e < e_hi) i = a.dst[e];
+      if (e >= e_lo && e < e_hi) i = a.dst[e];
     }
     uint32_t left = __ballot_sync(kFull, i >= 0);
     while (left) {
@@ -501,11 +597,11 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
       float2 w[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = left ? __ffs(left) - 1 : 0;
+        const int at = left ? __ffs(left) - 1 : 0;
         const bool on = left != 0;
         left &= left - 1;
-        const int64_t r = __shfl_sync(kFull, i, t);
-        const int64_t ee = __shfl_sync(kFull, e, t);
+        const int64_t r = __shfl_sync(kFull, i, at);
+        const int64_t ee = __shfl_sync(kFull, e, at);
         w[u] = make_float2(0.0f, 0.0f);
         if (on && L.live) w[u] = a.rec[ee * a.H + L.h];
 #pragma unroll
@@ -527,9 +623,9 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
     }
   }
   if constexpr (!WIDE) {
-    if (a.W > 1) {
+    if (t.W > 1) {
       const int warp = threadIdx.x >> 5;
-      if (L.split > 0) {
+      if (t.split > 0) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -539,8 +635,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
           }
       }
       __syncthreads();
-      if (L.split > 0) return;
-      for (int o = 1; o < a.W; ++o)
+      for (int o = 1; t.split == 0 && o < t.W; ++o)
 #pragma unroll
         for (int s = 0; s < S; ++s)
 #pragma unroll
@@ -550,16 +645,119 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
           }
     }
   }
-  if (!L.live) return;
+  if (L.live && t.split == 0) {
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (a.gk && L.oq[s] >= 0) {
+    for (int s = 0; s < S; ++s) {
+      if (t.part) {
+        if (L.oq[s] >= 0) store_vec<V>(t.part + L.oq[s], ak[s]);
+        if (L.ov[s] >= 0) store_vec<V>(t.part + a.dq + L.ov[s], av[s]);
+        continue;
+      }
+      if (a.gk && L.oq[s] >= 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) ak[s].x[i] *= a.scale;
-      store_vec<V>(a.gk + (int64_t)L.row * a.ldgk + L.oq[s], ak[s]);
+        for (int i = 0; i < V; ++i) ak[s].x[i] *= a.scale;
+        store_vec<V>(a.gk + (int64_t)t.row * a.ldgk + L.oq[s], ak[s]);
+      }
+      if (a.gv && L.ov[s] >= 0) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + L.ov[s], av[s]);
     }
-    if (a.gv && L.ov[s] >= 0) store_vec<V>(a.gv + (int64_t)L.row * a.ldgv + L.ov[s], av[s]);
   }
+  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
+  }
+}
+
+// Joins the partial rows of the long rows, in window order: CTA w acts when such a row begins in window w.
+// Its eight warps take every eighth window, 128 floats of the row at a time, and are then added up in
+// order.  Forward: the windows' sums meet at their common maximum.  Bound by the reads of the partials,
+// one row for `win` edges' gathers of two.
+constexpr int kJoinThreads = 256;
+
+template <int PASS>   // 0: y, lse; 1: gq; 2: gk, gv
+__device__ __forceinline__ void join_long_row(const AttnArgs& a, int w) {
+  __shared__ float top[32], total[32], sums[kJoinThreads / 32][128];
+  const int32_t* ptr = PASS == 2 ? a.colptr : a.rowptr;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32;
+  const int first = w * a.win, end = min(first + a.win, a.E);
+  const int row = find_row(ptr, a.N, end - 1);
+  if (row < 0) return;
+  const int start = __ldg(ptr + row), stop = min(__ldg(ptr + row + 1), a.E);
+  if (start < first || __ldg(ptr + row + 1) - start <= a.hub) return;
+  const int n = (stop - 1) / a.win - w + 1;             // windows w .. w + n - 1; only the first may be slot 1
+  auto part = [&](int i) {
+    return a.part + ((int64_t)(w + i) * 2 + (i == 0 && start > first ? 1 : 0)) * a.part_len;
+  };
+  if (PASS == 0) {
+    for (int h = warp; h < a.H; h += warps) {
+      float m = -INFINITY, l = 0.0f;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[a.part_len - 2 * a.H + h]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      const float ref = m == -INFINITY ? 0.0f : m;
+      for (int i = lane; i < n; i += 32) {
+        const float* p = part(i) + a.part_len - 2 * a.H + h;
+        l += p[a.H] * exp_of(p[0] - ref);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+      if (lane == 0) {
+        top[h] = ref;
+        const bool none = m == -INFINITY && l == 0.0f;
+        total[h] = none ? 0.0f : a.drop.inv_keep / l;
+        if (a.lse) a.lse[(int64_t)row * a.H + h] = none ? -INFINITY : m + logf(l);
+      }
+    }
+    __syncthreads();
+  }
+  const int width = PASS == 0 ? a.dv : PASS == 1 ? a.dq : a.dq + a.dv;
+  for (int d0 = 0; d0 < width; d0 += 128) {
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int head[4] = {0, 0, 0, 0};
+    if (PASS == 0) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int d = min(d0 + c * 32 + lane, width - 1);
+        int b = a.mv.nb - 1;
+        while (b > 0 && d < a.mv.off[b]) --b;
+        head[c] = (d - a.mv.off[b]) / a.mv.len[b];
+      }
+    }
+#pragma unroll 4
+    for (int i = warp; i < n; i += warps) {
+      const float* p = part(i);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int d = d0 + c * 32 + lane;
+        if (d >= width) continue;
+        const float f = PASS == 0 ? exp_of(p[a.part_len - 2 * a.H + head[c]] - top[head[c]]) : 1.0f;
+        t[c] = fmaf(f, p[d], t[c]);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sums[warp][c * 32 + lane] = t[c];
+    __syncthreads();
+    const int d = d0 + threadIdx.x;
+    if (threadIdx.x < 128 && d < width) {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kJoinThreads / 32; ++i) v += sums[i][threadIdx.x];
+      if (PASS == 0) {
+        int b = a.mv.nb - 1;
+        while (b > 0 && d < a.mv.off[b]) --b;
+        a.y[(int64_t)row * a.dv + d] = v * total[(d - a.mv.off[b]) / a.mv.len[b]];
+      } else if (PASS == 1) {
+        a.gq[(int64_t)row * a.ldgq + d] = a.scale * v;
+      } else if (d < a.dq) {
+        if (a.gk) a.gk[(int64_t)row * a.ldgk + d] = a.scale * v;
+      } else if (a.gv) {
+        a.gv[(int64_t)row * a.ldgv + d - a.dq] = v;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <int PASS>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a) {
+  join_long_row<PASS>(a, blockIdx.x);
 }
 
 // gtable[b, h] = sum of ds over the edges of bucket b.  The edges are cut into contiguous ranges, one
@@ -659,7 +857,8 @@ void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
     a.hw = 1;
     a.groups = a.H;
     a.W = 1;
-    const unsigned grid = (unsigned)((int64_t)a.N * a.H);
+    a.row_ctas = a.N * a.H;
+    const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
     switch (slots_for((chunks + threads - 1) / threads, true)) {
       case 2: return launch_one<V, 2, 4, true>(pass, a, grid, threads, s);
       case 4: return launch_one<V, 4, 2, true>(pass, a, grid, threads, s);
@@ -676,7 +875,8 @@ void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   a.W = 1;
   while (a.W < kAttnWarps && units * a.W < 148 * 24 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
   const int per = kAttnWarps / a.W;
-  const unsigned grid = (unsigned)((units + per - 1) / per);
+  a.row_ctas = (int)((units + per - 1) / per);
+  const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
   switch (slots_for(need, false)) {
     case 1: return launch_one<V, 1, 4, false>(pass, a, grid, kAttnThreads, s);
     case 2: return launch_one<V, 2, 4, false>(pass, a, grid, kAttnThreads, s);
@@ -687,9 +887,32 @@ void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_pass(Pass pass, AttnArgs& a, bool vec4, cudaStream_t s) {
+// Windows of at least 128 edges, and no more of them than 16 a SM: rows of up to twice that stay with
+// their own warps.
+void window_plan(AttnArgs& a) {
+  a.win = std::max(kMinWindow, (a.E / (148 * 16) + 32) / 32 * 32);
+  a.hub = 2 * a.win;
+  a.n_win = a.E > a.hub ? (a.E + a.win - 1) / a.win : 0;
+}
+
+int part_len(const AttnArgs& a, Pass pass) {
+  const int n = pass == kFwd ? a.dv + 2 * a.H : pass == kRecv ? a.dq : a.dq + a.dv;
+  return (n + 3) & ~3;
+}
+
+size_t part_bytes(const AttnArgs& a, Pass pass) { return sizeof(float) * 2 * (size_t)a.n_win * part_len(a, pass); }
+
+cudaError_t launch_pass(Pass pass, AttnArgs& a, bool vec4, float* part, cudaStream_t s) {
+  a.part = part;
+  a.part_len = part_len(a, pass);
   if (vec4) launch_slots<4>(pass, a, s);
   else launch_slots<1>(pass, a, s);
+  count_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.n_win == 0 || (pass == kRecv && !a.gq)) return e;
+  if (pass == kFwd) k_attn_join<0><<<a.n_win, kJoinThreads, 0, s>>>(a);
+  else if (pass == kRecv) k_attn_join<1><<<a.n_win, kJoinThreads, 0, s>>>(a);
+  else k_attn_join<2><<<a.n_win, kJoinThreads, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -717,7 +940,7 @@ struct tp_attn_s {
 namespace {
 
 struct BwdLayout {
-  size_t rec, dst, hist, colptr, perm, scratch, total;
+  size_t rec, dst, hist, colptr, perm, scratch, part, total;
 };
 
 BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
@@ -725,6 +948,7 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   a.N = (int)N;
   a.E = (int)E;
   hist_plan(a);
+  window_plan(a);
   BwdLayout L;
   size_t off = 0;
   const size_t e = (size_t)std::max<int64_t>(E, 1);
@@ -740,6 +964,8 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   off += al256(sizeof(int32_t) * e);
   L.scratch = off;
   off += al256(sizeof(int32_t) * (size_t)transpose_scratch_ints(N, E));
+  L.part = off;              // the receiver pass's and the sender pass's in turn
+  off += al256(std::max(part_bytes(a, kRecv), part_bytes(a, kSend)));
   L.total = off;
   return L;
 }
@@ -747,8 +973,8 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
 tp_status_t attn_sizes(tp_attn_t h, int64_t N, int64_t E) {
   if (!h) return set_failure(TP_ERR_INVALID_ARG, "attention is NULL");
   if (N < 0 || E < 0) return set_failure(TP_ERR_INVALID_ARG, "N and E must be non-negative");
-  if (E > 0x7fffffff - 64 || N * h->proto.H > 0x7fffffff - 64)
-    return set_failure(TP_ERR_UNSUPPORTED, "E and N * heads must stay below 2^31 - 64 (int32 indices)");
+  if (E > 0x7fffffff - (1 << 22) || N * h->proto.H > 0x7fffffff - (1 << 22))
+    return set_failure(TP_ERR_UNSUPPORTED, "E and N * heads must stay below 2^31 - 2^22 (int32 indices)");
   return TP_OK;
 }
 
@@ -783,6 +1009,7 @@ tp_status_t attn_inputs(tp_attn_t h, int64_t N, int64_t E, const int32_t* rowptr
   a.ldv = ldv;
   a.table = table;
   a.scale = scale;
+  window_plan(a);
   return TP_OK;
 }
 
@@ -869,7 +1096,10 @@ tp_status_t tp_attn_workspace_size(tp_attn_t attn, int64_t N, int64_t E, int32_t
   if (st != TP_OK) return st;
   if (!bytes) return set_failure(TP_ERR_INVALID_ARG, "bytes is NULL");
   if (op != TP_OP_FWD && op != TP_OP_BWD) return set_failure(TP_ERR_INVALID_ARG, "op must be TP_OP_FWD or TP_OP_BWD");
-  *bytes = op == TP_OP_FWD ? 0 : bwd_layout(attn, N, E).total;
+  AttnArgs a = attn->proto;
+  a.E = (int)E;
+  window_plan(a);
+  *bytes = op == TP_OP_FWD ? al256(part_bytes(a, kFwd)) : bwd_layout(attn, N, E).total;
   return TP_OK;
 }
 
@@ -885,11 +1115,13 @@ tp_status_t tp_attn_fwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   if (st != TP_OK) return st;
   if (!y) return set_failure(TP_ERR_INVALID_ARG, "y must not be NULL");
   if (!al4(y) || !al4(lse)) return set_failure(TP_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
-  (void)ws;
-  (void)ws_bytes;
+  const size_t need = part_bytes(a, kFwd);
+  if (need > 0 && (!ws || ws_bytes < need)) return set_failure(TP_ERR_WORKSPACE, "workspace too small");
+  if (need > 0 && (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return set_failure(TP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   a.y = y;
   a.lse = lse;
-  return cuda_status(launch_pass(kFwd, a, attn->vec4 && rows4(a) && al16(y), reinterpret_cast<cudaStream_t>(stream)),
+  return cuda_status(launch_pass(kFwd, a, attn->vec4 && rows4(a) && al16(y), static_cast<float*>(ws), reinterpret_cast<cudaStream_t>(stream)),
                      "tp_attn_fwd");
 }
 
@@ -956,8 +1188,9 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   a.hist = reinterpret_cast<float*>(w + L.hist);
   const bool vec4 = attn->vec4 && rows4(a) && al16(y) && al16(gy) && al16(gq) && al16(gk) && al16(gv) &&
                     (!gq || ldgq % 4 == 0) && (!gk || ldgk % 4 == 0) && (!gv || ldgv % 4 == 0);
-  e = launch_pass(kRecv, a, vec4, s);
-  if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, s);
+  float* part = reinterpret_cast<float*>(w + L.part);
+  e = launch_pass(kRecv, a, vec4, part, s);
+  if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, part, s);
   if (e == cudaSuccess && gtable && E > 0) {
     hist_plan(a);
     const size_t smem = sizeof(float) * (size_t)a.K * a.H * a.hist_copies;
