@@ -7,16 +7,21 @@
 // shuffles.  A warp holds 32 / G heads of one receiver; heads beyond 1,024 floats take a whole
 // CTA (WIDE), whose dot products are joined through shared memory.
 //
-// Forward and the receiver pass of the backward walk the edges of a receiver: the senders and
-// buckets of 32 edges are read by the 32 lanes, edges that take no part are struck out by a
-// ballot, and the rest goes U edges at a time, with all 2 U row gathers issued before the first
-// use.  The softmax runs in one pass with the running maximum and sum.
+// A warp takes the edges of a receiver 32 at a time.  One lane reads one edge (sender, bucket,
+// dropout choices); edges that take no part are struck out and the rest is closed up in shared
+// memory.  Forward, per batch: (a) the logits, U edges at a time, each lane's chunks of U rows of k
+// in flight at once; (b) the softmax of the batch with one lane per edge and head -- bias, running
+// maximum, exp and sum cost a few instructions per edge there, where doing them for every edge in
+// every lane of its group cost more than the products; (c) the sum of p v, again U rows at a time.
+// The receiver pass of the backward needs no running maximum (p = exp(s - lse)), so it keeps the
+// rows of k in registers between the logit and gq and walks the edges once.  The sender pass
+// finds (ds, r p) in the workspace and only adds up.
 //
 // Long rows.  A receiver (sender) of more than `hub` edges would keep one warp busy long after the
 // others are done.  Its edges are taken window by window instead: the edge axis is cut into
 // windows of win = hub / 2 edges, one CTA each, behind the CTAs of the rows.  A window meets at
 // most two such rows (the row of its first edge and the row of its last one), finds them by a
-// 33-way search in the row pointers and leaves a partial row for each; k_attn_join adds a row's
+// 33-way search in the row pointers and leaves a partial row for each; a join kernel adds a row's
 // partials up in window order.  Graphs of at most `hub` edges have neither windows nor the join.
 #include <algorithm>
 #include <cmath>
@@ -62,7 +67,7 @@ struct AttnArgs {
   const float* q;
   const float* k;
   const float* v;
-  int64_t ldq, ldk, ldv;
+  uint32_t ldq, ldk, ldv;    // row strides in bytes
   const float* table;
   float scale;
   DropArgs drop;
@@ -74,16 +79,22 @@ struct AttnArgs {
   float* gq;
   float* gk;
   float* gv;
-  int64_t ldgq, ldgk, ldgv;
+  int64_t ldgq, ldgk, ldgv;  // in floats
   float* gtable;
   float2* rec;               // workspace [E][H]: (ds, r p) of the backward pass
   int32_t* dst;              // workspace [E]: receiver, -1 for an edge that takes no part
   float* hist;               // workspace [hist_ctas][K * H]
-  int hist_ctas, hist_copies, hist_lanes;
+  int hist_ctas, hist_copies, hist_lanes;   // hist_ctas = 0 in the sender pass: no table CTAs behind it
   HeadMap mq, mv;
 };
 
 constexpr int kMinWindow = 128;
+
+// The kernels of one call follow each other by programmatic dependent launch: a kernel lets the next
+// one be set up from its start on, and the next one waits here, before it touches anything that an
+// earlier one writes, until all of them are done.
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ int slot_offset(const HeadMap& m, int h, int pos) {
   for (int b = 0; b < m.nb; ++b) {
@@ -99,19 +110,32 @@ struct Vec {
 };
 
 template <int V>
-__device__ __forceinline__ Vec<V> load_vec(const float* p, bool on) {
+__device__ __forceinline__ Vec<V> zero_vec() {
   Vec<V> r;
 #pragma unroll
   for (int i = 0; i < V; ++i) r.x[i] = 0.0f;
-  if (on) {
+  return r;
+}
+
+// Reads a chunk.  GUARD: a lane without one (on = false) gets zeros.
+template <int V, bool GUARD>
+__device__ __forceinline__ Vec<V> load_vec(const char* p, bool on) {
+  Vec<V> r;
+  if constexpr (GUARD) r = zero_vec<V>();
+  if (!GUARD || on) {
     if constexpr (V == 4) {
       const float4 t = __ldg(reinterpret_cast<const float4*>(p));
       r.x[0] = t.x, r.x[1] = t.y, r.x[2] = t.z, r.x[3] = t.w;
     } else {
-      r.x[0] = __ldg(p);
+      r.x[0] = __ldg(reinterpret_cast<const float*>(p));
     }
   }
   return r;
+}
+
+// Byte address of row j for a lane's chunk: one 32 x 32 -> 64 bit multiply-add.
+__device__ __forceinline__ const char* row_at(const char* p, int j, uint32_t row_bytes) {
+  return p + (uint64_t)(uint32_t)j * row_bytes;
 }
 
 template <int V>
@@ -221,12 +245,12 @@ struct Tasks {
   }
 };
 
-// Which head and chunks of the task's row a thread holds.
-template <int V, int S, bool WIDE>
+// Which head of the task's row a thread holds, and its chunks: number s G + gl of the head's chunks.
+// Lanes beyond the last head shadow it; `live` keeps what they find out of every output.
+template <int V, bool WIDE>
 struct Lane {
   int h, G, gl, sub;
-  bool live;                 // the lane holds a head of a row
-  int oq[S], ov[S];
+  bool live;
 
   __device__ __forceinline__ Lane(const AttnArgs& a, const Task& t) {
     const int lane = threadIdx.x & 31;
@@ -235,20 +259,28 @@ struct Lane {
       sub = 0;
       G = blockDim.x;
       gl = threadIdx.x;
+      live = t.write;
     } else {
       G = 32 / a.hw;
       sub = lane / G;
       gl = lane & (G - 1);
       h = t.head0 + sub;
-    }
-    live = t.write && t.row < a.N && h < a.H;
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int pos = (s * G + gl) * V;
-      oq[s] = live ? slot_offset(a.mq, h, pos) : -1;
-      ov[s] = live ? slot_offset(a.mv, h, pos) : -1;
+      live = t.write && h < a.H;
+      h = min(h, a.H - 1);
     }
   }
+
+  __device__ __forceinline__ bool has(const HeadMap& m, int s) const { return (s * G + gl) * V < m.hd; }
+  // Offsets of the chunks in a row; a chunk the lane lacks is given the row's first float.
+  template <int S>
+  __device__ __forceinline__ void offsets(const HeadMap& m, int (&o)[S]) const {
+#pragma unroll
+    for (int s = 0; s < S; ++s) o[s] = max(slot_offset(m, h, (s * G + gl) * V), 0);
+  }
+
+  // The lane's part in a batch of 32 edges x the warp's heads: entries lane' + 32 i of [edge][head].
+  __device__ __forceinline__ int step() const { return WIDE ? 32 : G; }
+  __device__ __forceinline__ int first() const { return WIDE ? (int)(threadIdx.x & 31) : gl; }
 
   // Sums of U values over the group, in every lane of it.  WIDE: `buf` holds [2][warps][U], used in turn.
   template <int U>
@@ -309,359 +341,561 @@ __device__ __forceinline__ EdgeLane read_edge(const AttnArgs& a, const DropKey& 
   return r;
 }
 
-template <int V, int S, int U, bool WIDE>
+// A warp's place in shared memory for a batch: the live edges' rows, two more words of each, and two
+// floats per edge and head.
+struct Batch {
+  int* row;
+  int* b;
+  uint32_t* c;
+  float* f;                  // [32][hw] floats, or float2
+};
+
+__device__ __forceinline__ Batch batch_of_warp(int hw) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  int* p = reinterpret_cast<int*>(dyn) + (threadIdx.x >> 5) * (96 + 64 * hw);
+  return Batch{p, p + 32, reinterpret_cast<uint32_t*>(p + 64), reinterpret_cast<float*>(p + 96)};
+}
+size_t batch_bytes(int threads, int hw) { return (size_t)(threads / 32) * (96 + 64 * hw) * 4; }
+
+// An entry whose table value is -inf: its edge takes no part for that head, and no row of it may reach
+// a sum, whatever it holds.  Such an entry is marked with -0, which no probability is.
+__device__ __forceinline__ bool marked(float p) { return __float_as_uint(p) == 0x80000000u; }
+
+template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_fwd(const __grid_constant__ AttnArgs a) {
-  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * S + 2) * 32];
+  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * SV + 2) * 32];
+  let_next_launch();
   const int lane = threadIdx.x & 31;
+  const Batch B = batch_of_warp(a.hw);
   int turn = 0;
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
   const Tasks tasks(a, a.rowptr, WIDE);
   for (int task = 0; task < tasks.n; ++task) {
-  const Task t = tasks.get(a, a.rowptr, task, WIDE);
-  const Lane<V, S, WIDE> L(a, t);
-  Vec<V> q[S], acc[S];
-  float m = -INFINITY, l = 0.0f;
+    const Task t = tasks.get(a, a.rowptr, task, WIDE);
+    const Lane<V, WIDE> L(a, t);
+    Vec<V> q[SQ], acc[SV];
+    const char *kp[SQ], *vp[SV];
+    float m = -INFINITY, l = 0.0f;       // maximum of the group's logits; the lane's share of the sum
+    {
+      int oq[SQ], ov[SV];
+      L.offsets(a.mq, oq);
+      L.offsets(a.mv, ov);
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    q[s] = load_vec<V>(a.q + (int64_t)t.row * a.ldq + L.oq[s], L.oq[s] >= 0);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[s].x[i] = 0.0f;
-  }
-  for (int base = t.lo; base < t.hi; base += 32) {
-    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, WIDE ? 1 : a.hw);
-    uint32_t left = __ballot_sync(kFull, mine.j >= 0);
-    while (left) {
-      Vec<V> kk[U][S], vv[U][S];
-      float bias[U], dot[U];
-      bool kept[U], on[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = left ? __ffs(left) - 1 : 0;
-        on[u] = left != 0;
-        left &= left - 1;
-        const int64_t j = __shfl_sync(kFull, mine.j, at);
-        const int b = __shfl_sync(kFull, mine.b, at);
-        kept[u] = (__shfl_sync(kFull, mine.keep, at) >> L.sub) & 1u;
-#pragma unroll
-        for (int s = 0; s < S; ++s) kk[u][s] = load_vec<V>(a.k + j * a.ldk + L.oq[s], on[u] && L.oq[s] >= 0);
-#pragma unroll
-        for (int s = 0; s < S; ++s) vv[u][s] = load_vec<V>(a.v + j * a.ldv + L.ov[s], on[u] && L.ov[s] >= 0);
-        bias[u] = 0.0f;
-        if (a.table && on[u] && L.live) bias[u] = __ldg(a.table + (int64_t)b * a.H + L.h);
+      for (int s = 0; s < SQ; ++s) {
+        kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
+        q[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.q + oq[s]), t.row, a.ldq), L.live && L.has(a.mq, s));
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        dot[u] = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) dot[u] = fmaf(q[s].x[i], kk[u][s].x[i], dot[u]);
+      for (int s = 0; s < SV; ++s) {
+        vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
+        acc[s] = zero_vec<V>();
       }
-      L.sum(dot, join, turn);
-      float top = m;
+    }
+    for (int base = t.lo; base < t.hi; base += 32) {
+      const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, a.hw);
+      const uint32_t live = __ballot_sync(kFull, mine.j >= 0);
+      const int n = __popc(live);
+      if (n == 0) continue;
+      __syncwarp();
+      if (mine.j >= 0) {
+        const int at = __popc(live & ((1u << lane) - 1u));
+        B.row[at] = mine.j;
+        B.b[at] = mine.b;
+        B.c[at] = mine.keep;
+      }
+      __syncwarp();
+      // (a) logits.  The last round repeats the last edge where there are fewer than U left.
+      for (int t0 = 0; t0 < n; t0 += U) {
+        float dot[U];
+        Vec<V> x[U][SQ];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool out = !on[u] || bias[u] == -INFINITY;
-        dot[u] = out ? -INFINITY : fmaf(dot[u], a.scale, bias[u]);
-        if (out) {                       // a masked row may hold anything: 0 times it has to be 0
+        for (int u = 0; u < U; ++u) {
+          const int j = B.row[min(t0 + u, n - 1)];
 #pragma unroll
-          for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int i = 0; i < V; ++i) vv[u][s].x[i] = 0.0f;
+          for (int s = 0; s < SQ; ++s)
+            x[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(kp[s], j, a.ldk), true)
+                                           : load_vec<V, true>(row_at(kp[s], j, a.ldk), L.has(a.mq, s));
         }
-        top = fmaxf(top, dot[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          dot[u] = 0.0f;
+#pragma unroll
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[u] = fmaf(q[s].x[i], x[u][s].x[i], dot[u]);
+        }
+        L.sum(dot, join, turn);
+        if (L.first() == 0) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) B.f[min(t0 + u, n - 1) * a.hw + L.sub] = dot[u];
+        }
       }
+      __syncwarp();
+      // (b) softmax of the batch
+      float top = m;
+      bool any_out = false;
+      for (int i = L.first(); i < n; i += L.step()) {
+        float& f = B.f[i * a.hw + L.sub];
+        const float bias = a.table && L.live ? __ldg(a.table + (int64_t)B.b[i] * a.H + L.h) : 0.0f;
+        const bool out = bias == -INFINITY;
+        any_out |= out;
+        f = out ? -INFINITY : fmaf(f, a.scale, bias);
+        top = fmaxf(top, f);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (L.step() > o) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
       const float ref = top == -INFINITY ? 0.0f : top;
       const float shrink = exp_of(m - ref);
       m = top;
       l *= shrink;
 #pragma unroll
-      for (int s = 0; s < S; ++s)
+      for (int s = 0; s < SV; ++s)
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[s].x[i] *= shrink;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float p = exp_of(dot[u] - ref);
+      for (int i = L.first(); i < n; i += L.step()) {
+        float& f = B.f[i * a.hw + L.sub];
+        const bool out = any_out && f == -INFINITY;
+        const float p = exp_of(f - ref);
         l += p;
-        const float pr = kept[u] ? p : 0.0f;
+        f = out ? -0.0f : (B.c[i] >> L.sub) & 1u ? p : 0.0f;
+      }
+      any_out = __any_sync(kFull, any_out);
+      __syncwarp();
+      // (c) sum of p v
+      for (int t0 = 0; t0 < n; t0 += U) {
+        Vec<V> x[U][SV];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int u = 0; u < U; ++u) {
+          const int j = B.row[min(t0 + u, n - 1)];
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[s].x[i] = fmaf(pr, vv[u][s].x[i], acc[s].x[i]);
+          for (int s = 0; s < SV; ++s)
+            x[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(vp[s], j, a.ldv), true)
+                                           : load_vec<V, true>(row_at(vp[s], j, a.ldv), L.has(a.mv, s));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (t0 + u >= n) break;
+          const float p = B.f[(t0 + u) * a.hw + L.sub];
+          if (any_out && marked(p)) continue;
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[s].x[i] = fmaf(p, x[u][s].x[i], acc[s].x[i]);
+        }
       }
     }
-  }
-  if constexpr (!WIDE) {
-    if (t.W > 1) {                       // join the warps of a row in order
-      const int warp = threadIdx.x >> 5;
-      float* mine = join + warp * (V * S + 2) * 32;
-      if (t.split > 0) {
-        mine[lane] = m;
-        mine[32 + lane] = l;
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+    for (int o = 16; o > 0; o >>= 1)
+      if (L.step() > o) l += __shfl_xor_sync(kFull, l, o);
+    if constexpr (!WIDE) {
+      if (t.W > 1) {                       // join the warps of a row in order
+        const int warp = threadIdx.x >> 5;
+        float* mine = join + warp * (V * SV + 2) * 32;
+        if (t.split > 0) {
+          mine[lane] = m;
+          mine[32 + lane] = l;
 #pragma unroll
-          for (int i = 0; i < V; ++i) mine[(2 + s * V + i) * 32 + lane] = acc[s].x[i];
-      }
-      __syncthreads();
-      for (int w = 1; t.split == 0 && w < t.W; ++w) {
-        const float* other = join + (warp + w) * (V * S + 2) * 32;
-        const float m2 = other[lane], top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
-        const float f1 = exp_of(m - ref), f2 = exp_of(m2 - ref);
-        l = l * f1 + other[32 + lane] * f2;
+          for (int s = 0; s < SV; ++s)
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+            for (int i = 0; i < V; ++i) mine[(2 + s * V + i) * 32 + lane] = acc[s].x[i];
+        }
+        __syncthreads();
+        for (int w = 1; t.split == 0 && w < t.W; ++w) {
+          const float* other = join + (warp + w) * (V * SV + 2) * 32;
+          const float m2 = other[lane], top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top;
+          const float f1 = exp_of(m - ref), f2 = exp_of(m2 - ref);
+          l = l * f1 + other[32 + lane] * f2;
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[s].x[i] = acc[s].x[i] * f1 + other[(2 + s * V + i) * 32 + lane] * f2;
-        m = top;
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[s].x[i] = acc[s].x[i] * f1 + other[(2 + s * V + i) * 32 + lane] * f2;
+          m = top;
+        }
       }
     }
-  }
-  if (L.live && t.split == 0) {
-    if (t.part) {
+    if (L.live && t.split == 0) {
+      int64_t ov[SV];
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (L.ov[s] >= 0) store_vec<V>(t.part + L.ov[s], acc[s]);
-      if (L.gl == 0) {
-        t.part[a.part_len - 2 * a.H + L.h] = m;
-        t.part[a.part_len - a.H + L.h] = l;
+      for (int s = 0; s < SV; ++s) ov[s] = reinterpret_cast<const float*>(vp[s]) - a.v;
+      if (t.part) {
+#pragma unroll
+        for (int s = 0; s < SV; ++s)
+          if (L.has(a.mv, s)) store_vec<V>(t.part + ov[s], acc[s]);
+        if (L.gl == 0) {
+          t.part[a.part_len - 2 * a.H + L.h] = m;
+          t.part[a.part_len - a.H + L.h] = l;
+        }
+      } else {
+        const bool none = m == -INFINITY && l == 0.0f;
+        const float f = none ? 0.0f : a.drop.inv_keep / l;
+#pragma unroll
+        for (int s = 0; s < SV; ++s) {
+          if (!L.has(a.mv, s)) continue;
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[s].x[i] *= f;
+          store_vec<V>(a.y + (int64_t)t.row * a.dv + ov[s], acc[s]);
+        }
+        if (a.lse && L.gl == 0) a.lse[(int64_t)t.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
       }
-    } else {
-      const bool none = m == -INFINITY && l == 0.0f;
-      const float f = none ? 0.0f : a.drop.inv_keep / l;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        if (L.ov[s] < 0) continue;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[s].x[i] *= f;
-        store_vec<V>(a.y + (int64_t)t.row * a.dv + L.ov[s], acc[s]);
-      }
-      if (a.lse && L.gl == 0) a.lse[(int64_t)t.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
     }
-  }
-  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
+    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
-// Backward, receiver order: gq, and for the sender pass and gtable (ds, r p) of every edge and head
+// Backward, receiver order: gq, and for the sender pass and gtable (ds, r p) of every live edge and head
 // and the receiver of every edge.
-template <int V, int S, int U, bool WIDE>
+template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_recv(const __grid_constant__ AttnArgs a) {
-  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * 2 * U : kAttnWarps * V * S * 32];
+  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * 2 * U : kAttnWarps * V * SQ * 32];
+  let_next_launch();
   const int lane = threadIdx.x & 31;
+  const Batch B = batch_of_warp(a.hw);
+  float2* const w2 = reinterpret_cast<float2*>(B.f);
   int turn = 0;
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
   const Tasks tasks(a, a.rowptr, WIDE);
   for (int task = 0; task < tasks.n; ++task) {
-  const Task t = tasks.get(a, a.rowptr, task, WIDE);
-  const Lane<V, S, WIDE> L(a, t);
-  Vec<V> q[S], gy[S], acc[S];
-  float delta[2 * U];
+    const Task t = tasks.get(a, a.rowptr, task, WIDE);
+    const Lane<V, WIDE> L(a, t);
+    Vec<V> q[SQ], gy[SV], acc[SQ];
+    const char *kp[SQ], *vp[SV];
+    float delta[2 * U];
 #pragma unroll
-  for (int u = 0; u < 2 * U; ++u) delta[u] = 0.0f;
+    for (int u = 0; u < 2 * U; ++u) delta[u] = 0.0f;
+    {
+      int oq[SQ], ov[SV];
+      L.offsets(a.mq, oq);
+      L.offsets(a.mv, ov);
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    q[s] = load_vec<V>(a.q + (int64_t)t.row * a.ldq + L.oq[s], L.oq[s] >= 0);
-    gy[s] = load_vec<V>(a.gy + (int64_t)t.row * a.dv + L.ov[s], L.ov[s] >= 0);
-    const Vec<V> y = load_vec<V>(a.y_in + (int64_t)t.row * a.dv + L.ov[s], L.ov[s] >= 0);
+      for (int s = 0; s < SQ; ++s) {
+        kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
+        q[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.q + oq[s]), t.row, a.ldq), L.live && L.has(a.mq, s));
+        acc[s] = zero_vec<V>();
+      }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      acc[s].x[i] = 0.0f;
-      delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
+      for (int s = 0; s < SV; ++s) {
+        const bool on = L.live && L.has(a.mv, s);
+        vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
+        gy[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.gy + ov[s]), t.row, a.dv * 4u), on);
+        const Vec<V> y = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.y_in + ov[s]), t.row, a.dv * 4u), on);
+#pragma unroll
+        for (int i = 0; i < V; ++i) delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
+      }
     }
-  }
-  L.sum(delta, join, turn);
-  const float del = delta[0];
-  const float lse = L.live ? __ldg(a.lse_in + (int64_t)t.row * a.H + L.h) : 0.0f;
-  for (int base = t.lo; base < t.hi; base += 32) {
-    const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, WIDE ? 1 : a.hw);
-    if (a.rec && base + lane < t.hi && t.head0 == 0 && (!WIDE || threadIdx.x < 32))
-      a.dst[base + lane] = mine.j >= 0 ? t.row : -1;
-    if (a.rec && base + lane < t.hi && mine.j < 0 && (!WIDE || threadIdx.x < 32))
-      for (int h = t.head0; h < min(a.H, t.head0 + (WIDE ? 1 : a.hw)); ++h)
-        a.rec[(int64_t)(base + lane) * a.H + h] = make_float2(0.0f, 0.0f);
-    uint32_t left = __ballot_sync(kFull, mine.j >= 0);
-    while (left) {
-      Vec<V> kk[U][S], vv[U][S];
-      float bias[U], dot[2 * U];
-      bool kept[U], on[U];
-      int at[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        at[u] = left ? __ffs(left) - 1 : 0;
-        on[u] = left != 0;
-        left &= left - 1;
-        const int64_t j = __shfl_sync(kFull, mine.j, at[u]);
-        const int b = __shfl_sync(kFull, mine.b, at[u]);
-        kept[u] = (__shfl_sync(kFull, mine.keep, at[u]) >> L.sub) & 1u;
-#pragma unroll
-        for (int s = 0; s < S; ++s) kk[u][s] = load_vec<V>(a.k + j * a.ldk + L.oq[s], on[u] && L.oq[s] >= 0);
-#pragma unroll
-        for (int s = 0; s < S; ++s) vv[u][s] = load_vec<V>(a.v + j * a.ldv + L.ov[s], on[u] && L.ov[s] >= 0);
-        bias[u] = 0.0f;
-        if (a.table && on[u] && L.live) bias[u] = __ldg(a.table + (int64_t)b * a.H + L.h);
+    L.sum(delta, join, turn);
+    const float del = delta[0];
+    const float lse = L.live ? __ldg(a.lse_in + (int64_t)t.row * a.H + L.h) : 0.0f;
+    for (int base = t.lo; base < t.hi; base += 32) {
+      const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, a.hw);
+      if (a.rec && base + lane < t.hi && t.head0 == 0 && (!WIDE || threadIdx.x < 32))
+        a.dst[base + lane] = mine.j >= 0 ? t.row : -1;
+      const uint32_t live = __ballot_sync(kFull, mine.j >= 0);
+      const int n = __popc(live);
+      if (n == 0) continue;
+      __syncwarp();
+      const int at = __popc(live & ((1u << lane) - 1u));
+      if (mine.j >= 0) {
+        B.row[at] = mine.j;
+        B.b[at] = mine.b;
+        B.c[at] = mine.keep;
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        dot[u] = dot[U + u] = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            dot[u] = fmaf(q[s].x[i], kk[u][s].x[i], dot[u]);
-            dot[U + u] = fmaf(gy[s].x[i], vv[u][s].x[i], dot[U + u]);
-          }
+      __syncwarp();
+      bool any_out = false;              // bias and dropout factor, one lane per edge and head
+      for (int i = L.first(); i < n; i += L.step()) {
+        const float bias = a.table && L.live ? __ldg(a.table + (int64_t)B.b[i] * a.H + L.h) : 0.0f;
+        const bool out = bias == -INFINITY || lse == -INFINITY;
+        any_out |= out;
+        w2[i * a.hw + L.sub] = make_float2(out ? -INFINITY : bias - lse, (B.c[i] >> L.sub) & 1u ? a.drop.inv_keep : 0.0f);
       }
-      L.sum(dot, join, turn);
+      any_out = __any_sync(kFull, any_out);
+      __syncwarp();
+      if (mine.j >= 0) B.b[at] = base + lane;
+      for (int t0 = 0; t0 < n; t0 += U) {
+        float dot[2 * U];
+        Vec<V> kk[U][SQ], vv[U][SV];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool out = !on[u] || bias[u] == -INFINITY || lse == -INFINITY;
-        const float p = out ? 0.0f : exp_of(fmaf(dot[u], a.scale, bias[u]) - lse);
-        const float r = kept[u] ? a.drop.inv_keep : 0.0f;
-        const float ds = out ? 0.0f : p * (r * dot[U + u] - del);
-        if (out) {
+        for (int u = 0; u < U; ++u) {
+          const int j = B.row[min(t0 + u, n - 1)];
 #pragma unroll
-          for (int s = 0; s < S; ++s)
+          for (int s = 0; s < SQ; ++s)
+            kk[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(kp[s], j, a.ldk), true)
+                                            : load_vec<V, true>(row_at(kp[s], j, a.ldk), L.has(a.mq, s));
 #pragma unroll
-            for (int i = 0; i < V; ++i) kk[u][s].x[i] = 0.0f;
+          for (int s = 0; s < SV; ++s)
+            vv[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(vp[s], j, a.ldv), true)
+                                            : load_vec<V, true>(row_at(vp[s], j, a.ldv), L.has(a.mv, s));
         }
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int u = 0; u < U; ++u) {
+          dot[u] = dot[U + u] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[s].x[i] = fmaf(ds, kk[u][s].x[i], acc[s].x[i]);
-        if (a.rec && on[u] && L.live && L.gl == 0)
-          a.rec[(int64_t)(base + at[u]) * a.H + L.h] = make_float2(ds, p * r);
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[u] = fmaf(q[s].x[i], kk[u][s].x[i], dot[u]);
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) dot[U + u] = fmaf(gy[s].x[i], vv[u][s].x[i], dot[U + u]);
+        }
+        L.sum(dot, join, turn);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (t0 + u >= n) break;
+          float2& w = w2[(t0 + u) * a.hw + L.sub];
+          const bool out = any_out && w.x == -INFINITY;
+          const float p = out ? 0.0f : exp_of(fmaf(dot[u], a.scale, w.x));
+          const float pr = p * w.y, ds = out ? 0.0f : fmaf(pr, dot[U + u], -p * del);
+          __syncwarp();
+          if (L.first() == 0) w = make_float2(ds, out ? -0.0f : pr);
+          if (out) continue;
+#pragma unroll
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[s].x[i] = fmaf(ds, kk[u][s].x[i], acc[s].x[i]);
+        }
+      }
+      __syncwarp();
+      if (a.rec && L.live && (!WIDE || threadIdx.x < 32)) {
+        for (int i = L.first(); i < n; i += L.step()) {
+          a.rec[(int64_t)B.b[i] * a.H + L.h] = w2[i * a.hw + L.sub];
+        }
       }
     }
-  }
-  if constexpr (!WIDE) {
-    if (t.W > 1) {
-      const int warp = threadIdx.x >> 5;
-      if (t.split > 0) {
+    if constexpr (!WIDE) {
+      if (t.W > 1) {
+        const int warp = threadIdx.x >> 5;
+        if (t.split > 0) {
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+          for (int s = 0; s < SQ; ++s)
 #pragma unroll
-          for (int i = 0; i < V; ++i) join[(warp * S * V + s * V + i) * 32 + lane] = acc[s].x[i];
+            for (int i = 0; i < V; ++i) join[(warp * SQ * V + s * V + i) * 32 + lane] = acc[s].x[i];
+        }
+        __syncthreads();
+        for (int w = 1; t.split == 0 && w < t.W; ++w)
+#pragma unroll
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[s].x[i] += join[((warp + w) * SQ * V + s * V + i) * 32 + lane];
       }
-      __syncthreads();
-      for (int w = 1; t.split == 0 && w < t.W; ++w)
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) acc[s].x[i] += join[((warp + w) * S * V + s * V + i) * 32 + lane];
     }
-  }
-  if (L.live && t.split == 0 && a.gq) {
+    if (L.live && t.split == 0 && a.gq) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (L.oq[s] < 0) continue;
-      if (t.part) {
-        store_vec<V>(t.part + L.oq[s], acc[s]);
-        continue;
+      for (int s = 0; s < SQ; ++s) {
+        if (!L.has(a.mq, s)) continue;
+        const int64_t oq = reinterpret_cast<const float*>(kp[s]) - a.k;
+        if (t.part) {
+          store_vec<V>(t.part + oq, acc[s]);
+          continue;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[s].x[i] *= a.scale;
+        store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + oq, acc[s]);
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[s].x[i] *= a.scale;
-      store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + L.oq[s], acc[s]);
     }
-  }
-  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
+    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
+// gtable[b, h] = sum of ds over the edges of bucket b.  The edges are cut into contiguous ranges, one
+// for each group of lanes; a group's lanes own one head each and add into the group's own copy of the
+// table in shared memory, edge after edge, so every sum has a fixed order.  The reads of eight edges
+// are in flight before the first is added: with one at a time the three latencies of each edge were
+// all of the kernel (46,080 edges: 12 us).
+__device__ __forceinline__ void table_part(const AttnArgs& a, int cta) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  float* copies = reinterpret_cast<float*>(dyn);
+  const int KH = a.K * a.H, group = threadIdx.x / a.hist_lanes, h = threadIdx.x % a.hist_lanes;
+  for (int i = threadIdx.x; i < KH * a.hist_copies; i += blockDim.x) copies[i] = 0.0f;
+  __syncthreads();
+  const int lo = max(0, min(__ldg(a.rowptr), a.E)), hi = max(lo, min(__ldg(a.rowptr + a.N), a.E));
+  if (group < a.hist_copies && h < a.H) {
+    const int64_t ranges = (int64_t)a.hist_ctas * a.hist_copies, r = (int64_t)cta * a.hist_copies + group;
+    const int first = lo + (int)((hi - lo) * r / ranges), last = lo + (int)((hi - lo) * (r + 1) / ranges);
+    float* mine = copies + group * KH + h;
+    constexpr int kAhead = 8;
+    for (int e0 = first; e0 < last; e0 += kAhead) {
+      int b[kAhead], d[kAhead];
+      float ds[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = min(e0 + i, last - 1);
+        d[i] = a.dst[e];
+        b[i] = __ldg(a.bucket + e);
+        ds[i] = a.rec[(int64_t)e * a.H + h].x;
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (d[i] >= 0 && e0 + i < last) mine[b[i] * a.H] += ds[i];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < KH; i += blockDim.x) {
+    float t = 0.0f;
+    for (int c = 0; c < a.hist_copies; ++c) t += copies[c * KH + i];
+    (a.hist_ctas == 1 ? a.gtable : a.hist + (int64_t)cta * KH)[i] = t;
+  }
+}
+
+__global__ void __launch_bounds__(kAttnThreads) k_attn_table(const __grid_constant__ AttnArgs a) {
+  let_next_launch();
+  table_part(a, blockIdx.x);
+}
+
+// One warp per entry of gtable: the CTAs' partials in a fixed order, in 64 bits (a few hundred terms of
+// both signs).
+__device__ __forceinline__ void table_sum(const AttnArgs& a, int o) {
+  const int KH = a.K * a.H, lane = threadIdx.x & 31;
+  if (o >= KH) return;
+  double t = 0.0;
+#pragma unroll 4
+  for (int c = lane; c < a.hist_ctas; c += 32) t += (double)a.hist[(int64_t)c * KH + o];
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(kFull, t, s);
+  if (lane == 0) a.gtable[o] = (float)t;
+}
+
 // Backward, sender order: gk[j] = scale sum ds q[i], gv[j] = sum r p gy[i] over the edges that leave j.
-template <int V, int S, int U, bool WIDE>
+template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_send(const __grid_constant__ AttnArgs a) {
-  __shared__ float join[WIDE ? 1 : kAttnWarps * 2 * V * S * 32];
+  __shared__ float join[WIDE ? 1 : kAttnWarps * V * (SQ + SV) * 32];
+  let_next_launch();
+  if ((int)blockIdx.x >= a.row_ctas + a.n_win) {
+    wait_for_previous();
+    table_part(a, (int)blockIdx.x - a.row_ctas - a.n_win);
+    return;
+  }
   const int lane = threadIdx.x & 31;
+  const Batch B = batch_of_warp(a.hw);
+  float2* const w2 = reinterpret_cast<float2*>(B.f);
   const int e_lo = max(__ldg(a.rowptr), 0), e_hi = min(__ldg(a.rowptr + a.N), a.E);
   const Tasks tasks(a, a.colptr, WIDE);
+  wait_for_previous();
   for (int task = 0; task < tasks.n; ++task) {
-  const Task t = tasks.get(a, a.colptr, task, WIDE);
-  const Lane<V, S, WIDE> L(a, t);
-  Vec<V> ak[S], av[S];
+    const Task t = tasks.get(a, a.colptr, task, WIDE);
+    const Lane<V, WIDE> L(a, t);
+    Vec<V> ak[SQ], av[SV];
+    const char *qp[SQ], *gp[SV];
+    {
+      int oq[SQ], ov[SV];
+      L.offsets(a.mq, oq);
+      L.offsets(a.mv, ov);
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-#pragma unroll
-    for (int i = 0; i < V; ++i) ak[s].x[i] = av[s].x[i] = 0.0f;
-  for (int base = t.lo; base < t.hi; base += 32) {
-    int e = -1, i = -1;
-    if (base + lane < t.hi) {
-      e = __ldg(a.perm + base + lane);
-      if (e >= e_lo && e < e_hi) i = a.dst[e];
-    }
-    uint32_t left = __ballot_sync(kFull, i >= 0);
-    while (left) {
-      Vec<V> qq[U][S], gg[U][S];
-      float2 w[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int at = left ? __ffs(left) - 1 : 0;
-        const bool on = left != 0;
-        left &= left - 1;
-        const int64_t r = __shfl_sync(kFull, i, at);
-        const int64_t ee = __shfl_sync(kFull, e, at);
-        w[u] = make_float2(0.0f, 0.0f);
-        if (on && L.live) w[u] = a.rec[ee * a.H + L.h];
-#pragma unroll
-        for (int s = 0; s < S; ++s) qq[u][s] = load_vec<V>(a.q + r * a.ldq + L.oq[s], on && L.oq[s] >= 0);
-#pragma unroll
-        for (int s = 0; s < S; ++s) gg[u][s] = load_vec<V>(a.gy + r * a.dv + L.ov[s], on && L.ov[s] >= 0);
+      for (int s = 0; s < SQ; ++s) {
+        qp[s] = reinterpret_cast<const char*>(a.q + oq[s]);
+        ak[s] = zero_vec<V>();
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (w[u].x == 0.0f && w[u].y == 0.0f) continue;     // no part of this head: 0 times its rows is 0
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i2 = 0; i2 < V; ++i2) {
-            ak[s].x[i2] = fmaf(w[u].x, qq[u][s].x[i2], ak[s].x[i2]);
-            av[s].x[i2] = fmaf(w[u].y, gg[u][s].x[i2], av[s].x[i2]);
-          }
+      for (int s = 0; s < SV; ++s) {
+        gp[s] = reinterpret_cast<const char*>(a.gy + ov[s]);
+        av[s] = zero_vec<V>();
       }
     }
-  }
-  if constexpr (!WIDE) {
-    if (t.W > 1) {
-      const int warp = threadIdx.x >> 5;
-      if (t.split > 0) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            join[((warp * 2 + 0) * S * V + s * V + i) * 32 + lane] = ak[s].x[i];
-            join[((warp * 2 + 1) * S * V + s * V + i) * 32 + lane] = av[s].x[i];
-          }
+    for (int base = t.lo; base < t.hi; base += 32) {
+      int e = -1, i = -1;
+      if (base + lane < t.hi) {
+        e = __ldg(a.perm + base + lane);
+        if (e >= e_lo && e < e_hi) i = a.dst[e];
       }
-      __syncthreads();
-      for (int o = 1; t.split == 0 && o < t.W; ++o)
+      const uint32_t live = __ballot_sync(kFull, i >= 0);
+      const int n = __popc(live);
+      if (n == 0) continue;
+      __syncwarp();
+      if (i >= 0) {
+        const int at = __popc(live & ((1u << lane) - 1u));
+        B.row[at] = i;
+        B.b[at] = e;
+      }
+      __syncwarp();
+      bool any_out = false;
+      for (int c = L.first(); c < n; c += L.step()) {
+        const float2 w = L.live ? a.rec[(int64_t)B.b[c] * a.H + L.h] : make_float2(0.0f, 0.0f);
+        any_out |= marked(w.y);
+        w2[c * a.hw + L.sub] = w;
+      }
+      any_out = __any_sync(kFull, any_out);
+      __syncwarp();
+      for (int t0 = 0; t0 < n; t0 += U) {
+        Vec<V> qq[U][SQ], gg[U][SV];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
+        for (int u = 0; u < U; ++u) {
+          const int r = B.row[min(t0 + u, n - 1)];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            ak[s].x[i] += join[(((warp + o) * 2 + 0) * S * V + s * V + i) * 32 + lane];
-            av[s].x[i] += join[(((warp + o) * 2 + 1) * S * V + s * V + i) * 32 + lane];
-          }
+          for (int s = 0; s < SQ; ++s)
+            qq[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(qp[s], r, a.ldq), true)
+                                            : load_vec<V, true>(row_at(qp[s], r, a.ldq), L.has(a.mq, s));
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+            gg[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(gp[s], r, a.dv * 4u), true)
+                                            : load_vec<V, true>(row_at(gp[s], r, a.dv * 4u), L.has(a.mv, s));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (t0 + u >= n) break;
+          const float2 w = w2[(t0 + u) * a.hw + L.sub];
+          if (any_out && marked(w.y)) continue;
+#pragma unroll
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int c = 0; c < V; ++c) ak[s].x[c] = fmaf(w.x, qq[u][s].x[c], ak[s].x[c]);
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int c = 0; c < V; ++c) av[s].x[c] = fmaf(w.y, gg[u][s].x[c], av[s].x[c]);
+        }
+      }
     }
-  }
-  if (L.live && t.split == 0) {
+    if constexpr (!WIDE) {
+      if (t.W > 1) {
+        const int warp = threadIdx.x >> 5;
+        constexpr int T = (SQ + SV) * V;
+        if (t.split > 0) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      if (t.part) {
-        if (L.oq[s] >= 0) store_vec<V>(t.part + L.oq[s], ak[s]);
-        if (L.ov[s] >= 0) store_vec<V>(t.part + a.dq + L.ov[s], av[s]);
-        continue;
-      }
-      if (a.gk && L.oq[s] >= 0) {
+          for (int s = 0; s < SQ; ++s)
 #pragma unroll
-        for (int i = 0; i < V; ++i) ak[s].x[i] *= a.scale;
-        store_vec<V>(a.gk + (int64_t)t.row * a.ldgk + L.oq[s], ak[s]);
+            for (int i = 0; i < V; ++i) join[(warp * T + s * V + i) * 32 + lane] = ak[s].x[i];
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) join[(warp * T + (SQ + s) * V + i) * 32 + lane] = av[s].x[i];
+        }
+        __syncthreads();
+        for (int o = 1; t.split == 0 && o < t.W; ++o) {
+#pragma unroll
+          for (int s = 0; s < SQ; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) ak[s].x[i] += join[((warp + o) * T + s * V + i) * 32 + lane];
+#pragma unroll
+          for (int s = 0; s < SV; ++s)
+#pragma unroll
+            for (int i = 0; i < V; ++i) av[s].x[i] += join[((warp + o) * T + (SQ + s) * V + i) * 32 + lane];
+        }
       }
-      if (a.gv && L.ov[s] >= 0) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + L.ov[s], av[s]);
     }
-  }
-  if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
+    if (L.live && t.split == 0) {
+#pragma unroll
+      for (int s = 0; s < SQ; ++s) {
+        if (!L.has(a.mq, s)) continue;
+        const int64_t oq = reinterpret_cast<const float*>(qp[s]) - a.q;
+        if (t.part) {
+          store_vec<V>(t.part + oq, ak[s]);
+        } else if (a.gk) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) ak[s].x[i] *= a.scale;
+          store_vec<V>(a.gk + (int64_t)t.row * a.ldgk + oq, ak[s]);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < SV; ++s) {
+        if (!L.has(a.mv, s)) continue;
+        const int64_t ov = reinterpret_cast<const float*>(gp[s]) - a.gy;
+        if (t.part) store_vec<V>(t.part + a.dq + ov, av[s]);
+        else if (a.gv) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + ov, av[s]);
+      }
+    }
+    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
@@ -672,28 +906,29 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 constexpr int kJoinThreads = 256;
 
 template <int PASS>   // 0: y, lse; 1: gq; 2: gk, gv
-__device__ __forceinline__ void join_long_row(const AttnArgs& a, int w) {
+__device__ __forceinline__ void join_long_row(const AttnArgs& a, int w, const float* parts, int part_len) {
   __shared__ float top[32], total[32], sums[kJoinThreads / 32][128];
   const int32_t* ptr = PASS == 2 ? a.colptr : a.rowptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32;
   const int first = w * a.win, end = min(first + a.win, a.E);
-  const int row = find_row(ptr, a.N, end - 1);
+  const int row = find_row(ptr, a.N, end - 1);   // the row pointers are the caller's: read before the wait
+  wait_for_previous();
   if (row < 0) return;
   const int start = __ldg(ptr + row), stop = min(__ldg(ptr + row + 1), a.E);
   if (start < first || __ldg(ptr + row + 1) - start <= a.hub) return;
   const int n = (stop - 1) / a.win - w + 1;             // windows w .. w + n - 1; only the first may be slot 1
   auto part = [&](int i) {
-    return a.part + ((int64_t)(w + i) * 2 + (i == 0 && start > first ? 1 : 0)) * a.part_len;
+    return parts + ((int64_t)(w + i) * 2 + (i == 0 && start > first ? 1 : 0)) * part_len;
   };
   if (PASS == 0) {
     for (int h = warp; h < a.H; h += warps) {
       float m = -INFINITY, l = 0.0f;
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[a.part_len - 2 * a.H + h]);
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, part(i)[part_len - 2 * a.H + h]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
       const float ref = m == -INFINITY ? 0.0f : m;
       for (int i = lane; i < n; i += 32) {
-        const float* p = part(i) + a.part_len - 2 * a.H + h;
+        const float* p = part(i) + part_len - 2 * a.H + h;
         l += p[a.H] * exp_of(p[0] - ref);
       }
 #pragma unroll
@@ -727,7 +962,7 @@ __device__ __forceinline__ void join_long_row(const AttnArgs& a, int w) {
       for (int c = 0; c < 4; ++c) {
         const int d = d0 + c * 32 + lane;
         if (d >= width) continue;
-        const float f = PASS == 0 ? exp_of(p[a.part_len - 2 * a.H + head[c]] - top[head[c]]) : 1.0f;
+        const float f = PASS == 0 ? exp_of(p[part_len - 2 * a.H + head[c]] - top[head[c]]) : 1.0f;
         t[c] = fmaf(f, p[d], t[c]);
       }
     }
@@ -755,46 +990,26 @@ __device__ __forceinline__ void join_long_row(const AttnArgs& a, int w) {
   }
 }
 
-template <int PASS>
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnArgs a) {
-  join_long_row<PASS>(a, blockIdx.x);
+__global__ void __launch_bounds__(kJoinThreads) k_attn_fwd_join(const __grid_constant__ AttnArgs a) {
+  join_long_row<0>(a, blockIdx.x, a.part, a.part_len);
 }
 
-// gtable[b, h] = sum of ds over the edges of bucket b.  The edges are cut into contiguous ranges, one
-// for each group of lanes; a group's lanes own one head each and add into the group's own copy of the
-// table in shared memory, edge after edge, so every sum has a fixed order.
-__global__ void __launch_bounds__(kAttnThreads) k_attn_table(const __grid_constant__ AttnArgs a) {
-  extern __shared__ float copies[];
-  const int KH = a.K * a.H, group = threadIdx.x / a.hist_lanes, h = threadIdx.x % a.hist_lanes;
-  for (int i = threadIdx.x; i < KH * a.hist_copies; i += kAttnThreads) copies[i] = 0.0f;
-  __syncthreads();
-  const int lo = max(0, min(__ldg(a.rowptr), a.E)), hi = max(lo, min(__ldg(a.rowptr + a.N), a.E));
-  if (group < a.hist_copies && h < a.H) {
-    const int64_t ranges = (int64_t)a.hist_ctas * a.hist_copies, r = (int64_t)blockIdx.x * a.hist_copies + group;
-    const int first = lo + (int)((hi - lo) * r / ranges), last = lo + (int)((hi - lo) * (r + 1) / ranges);
-    float* mine = copies + group * KH;
-    for (int e = first; e < last; ++e) {
-      const int b = __ldg(a.bucket + e);
-      const float ds = a.rec[(int64_t)e * a.H + h].x;
-      if ((unsigned)b < (unsigned)a.K) mine[b * a.H + h] += ds;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < KH; i += kAttnThreads) {
-    float t = 0.0f;
-    for (int c = 0; c < a.hist_copies; ++c) t += copies[c * KH + i];
-    (a.hist_ctas == 1 ? a.gtable : a.hist + (int64_t)blockIdx.x * KH)[i] = t;
-  }
-}
+// What is left of a backward pass: the long rows of gq (CTAs 0 .. recv_joins - 1) and of gk and gv (the
+// next send_joins), and the sums of gtable's partials.
+struct Tail {
+  int recv_joins, send_joins;
+  float *recv_part, *send_part;
+  int recv_len, send_len;
+};
 
-__global__ void __launch_bounds__(128) k_attn_table_sum(const __grid_constant__ AttnArgs a) {
-  const int KH = a.K * a.H, o = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (o >= KH) return;
-  double t = 0.0;
-  for (int c = lane; c < a.hist_ctas; c += 32) t += (double)a.hist[(int64_t)c * KH + o];
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) t += __shfl_xor_sync(kFull, t, s);
-  if (lane == 0) a.gtable[o] = (float)t;
+__global__ void __launch_bounds__(kJoinThreads) k_attn_bwd_tail(const __grid_constant__ AttnArgs a, const __grid_constant__ Tail t) {
+  int cta = blockIdx.x;
+  if (cta < t.recv_joins) return join_long_row<1>(a, cta, t.recv_part, t.recv_len);
+  cta -= t.recv_joins;
+  if (cta < t.send_joins) return join_long_row<2>(a, cta, t.send_part, t.send_len);
+  cta -= t.send_joins;
+  wait_for_previous();
+  table_sum(a, cta * (kJoinThreads / 32) + (threadIdx.x >> 5));
 }
 
 // Distance buckets: squares in 64 bits (products of 32-bit floats are exact there), binary search.
@@ -834,23 +1049,54 @@ tp_status_t cuda_status(cudaError_t e, const char* where) {
 
 enum Pass { kFwd, kRecv, kSend };
 
-template <int V, int S, int U, bool WIDE>
-void launch_one(Pass pass, const AttnArgs& a, unsigned grid, int threads, cudaStream_t s) {
-  if (pass == kFwd) k_attn_fwd<V, S, U, WIDE><<<grid, threads, 0, s>>>(a);
-  else if (pass == kRecv) k_attn_bwd_recv<V, S, U, WIDE><<<grid, threads, 0, s>>>(a);
-  else k_attn_bwd_send<V, S, U, WIDE><<<grid, threads, 0, s>>>(a);
+// Launches `kernel` after the call's previous kernel (see let_next_launch).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-// Chunks a lane holds at most; the kernels exist for these counts.
-int slots_for(int need, bool wide) {
-  for (int s : {1, 2, 3, 4, 6, 8})
-    if (need <= s && !(wide && (s == 1 || s == 3 || s == 6))) return s;
-  return 0;
+// Shared memory of a table_part CTA.
+size_t hist_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H * a.hist_copies; }
+
+template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
+cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s) {
+  size_t smem = batch_bytes(threads, a.hw);
+  const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
+  if (pass == kSend) {
+    if (a.hist_ctas > 0) smem = std::max(smem, hist_bytes(a));
+    return launch_after(k_attn_bwd_send<V, SQ, SV, U, LOOSE, WIDE>, grid + (unsigned)a.hist_ctas, threads, smem, s, a);
+  }
+  if (pass == kFwd) k_attn_fwd<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
+  else k_attn_bwd_recv<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+// Three forms of the kernels for S chunks a lane: rows of q with a single chunk a lane (logits from a few
+// scalars), rows of q and v that both fill S - 1 chunks of every lane, and any others, where every read
+// asks whether the lane has the chunk.
+template <int V, int S, int U>
+cudaError_t launch_form(Pass pass, const AttnArgs& a, int cq, int cv, cudaStream_t s) {
+  const int G = 32 / a.hw, full = (S - 1) * G;
+  if (cv >= full && cq <= G) return launch_one<V, 1, S, U, false, false>(pass, a, kAttnThreads, s);
+  if (cv >= full && cq >= full) return launch_one<V, S, S, U, false, false>(pass, a, kAttnThreads, s);
+  return launch_one<V, S, S, U, true, false>(pass, a, kAttnThreads, s);
 }
 
 template <int V>
-void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
-  const int chunks = (std::max(a.mq.hd, a.mv.hd) + V - 1) / V;
+cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
+  const int cq = (a.mq.hd + V - 1) / V, cv = (a.mv.hd + V - 1) / V, chunks = std::max(cq, cv);
   if (chunks > 256) {
     int threads = 128;
     while (threads < kAttnWideThreads && (chunks + threads - 1) / threads > 4) threads *= 2;
@@ -858,12 +1104,8 @@ void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
     a.groups = a.H;
     a.W = 1;
     a.row_ctas = a.N * a.H;
-    const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
-    switch (slots_for((chunks + threads - 1) / threads, true)) {
-      case 2: return launch_one<V, 2, 4, true>(pass, a, grid, threads, s);
-      case 4: return launch_one<V, 4, 2, true>(pass, a, grid, threads, s);
-      default: return launch_one<V, 8, 1, true>(pass, a, grid, threads, s);
-    }
+    if (chunks <= 4 * threads) return launch_one<V, 4, 4, 2, true, true>(pass, a, threads, s);
+    return launch_one<V, 8, 8, 1, true, true>(pass, a, threads, s);
   }
   // as many heads in a warp as leave a lane at most four chunks
   int hw = 1;
@@ -873,17 +1115,17 @@ void launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   const int need = (chunks + 32 / hw - 1) / (32 / hw);
   const int64_t units = (int64_t)a.N * a.groups;
   a.W = 1;
-  while (a.W < kAttnWarps && units * a.W < 148 * 24 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
+  while (a.W < kAttnWarps && units * a.W < 148 * 8 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
   const int per = kAttnWarps / a.W;
   a.row_ctas = (int)((units + per - 1) / per);
-  const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
-  switch (slots_for(need, false)) {
-    case 1: return launch_one<V, 1, 4, false>(pass, a, grid, kAttnThreads, s);
-    case 2: return launch_one<V, 2, 4, false>(pass, a, grid, kAttnThreads, s);
-    case 3: return launch_one<V, 3, 2, false>(pass, a, grid, kAttnThreads, s);
-    case 4: return launch_one<V, 4, 2, false>(pass, a, grid, kAttnThreads, s);
-    case 6: return launch_one<V, 6, 1, false>(pass, a, grid, kAttnThreads, s);
-    default: return launch_one<V, 8, 1, false>(pass, a, grid, kAttnThreads, s);
+  switch (need) {
+    case 1: return launch_form<V, 1, 4>(pass, a, cq, cv, s);
+    case 2: return launch_form<V, 2, 4>(pass, a, cq, cv, s);
+    case 3: return launch_form<V, 3, 4>(pass, a, cq, cv, s);
+    case 4: return launch_form<V, 4, 2>(pass, a, cq, cv, s);
+    case 5:
+    case 6: return launch_form<V, 6, 1>(pass, a, cq, cv, s);
+    default: return launch_form<V, 8, 1>(pass, a, cq, cv, s);
   }
 }
 
@@ -905,25 +1147,17 @@ size_t part_bytes(const AttnArgs& a, Pass pass) { return sizeof(float) * 2 * (si
 cudaError_t launch_pass(Pass pass, AttnArgs& a, bool vec4, float* part, cudaStream_t s) {
   a.part = part;
   a.part_len = part_len(a, pass);
-  if (vec4) launch_slots<4>(pass, a, s);
-  else launch_slots<1>(pass, a, s);
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_win == 0 || (pass == kRecv && !a.gq)) return e;
-  if (pass == kFwd) k_attn_join<0><<<a.n_win, kJoinThreads, 0, s>>>(a);
-  else if (pass == kRecv) k_attn_join<1><<<a.n_win, kJoinThreads, 0, s>>>(a);
-  else k_attn_join<2><<<a.n_win, kJoinThreads, 0, s>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
+  return vec4 ? launch_slots<4>(pass, a, s) : launch_slots<1>(pass, a, s);
 }
 
+// Copies of the table per CTA: one per group of lanes while they fit 32 KB, at least one.
 void hist_plan(AttnArgs& a) {
   a.hist_lanes = 1;
   while (a.hist_lanes < a.H) a.hist_lanes *= 2;
   const int KH = std::max(1, a.K * a.H);
-  a.hist_copies = std::max(1, std::min(kAttnThreads / a.hist_lanes, 24 * 1024 / KH));
+  a.hist_copies = std::max(1, std::min(kAttnThreads / a.hist_lanes, 8 * 1024 / KH));
   // a CTA zeroes, sums and writes KH floats: give it at least as many edges' values
-  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(1024, KH / a.H * 4));
+  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(a.hist_copies * 16, KH / a.H * 4));
   a.hist_ctas = (int)std::min<int64_t>(want, 148 * 2);
 }
 
@@ -940,7 +1174,7 @@ struct tp_attn_s {
 namespace {
 
 struct BwdLayout {
-  size_t rec, dst, hist, colptr, perm, scratch, part, total;
+  size_t rec, dst, hist, colptr, perm, scratch, recv_part, send_part, total;
 };
 
 BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
@@ -964,8 +1198,10 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   off += al256(sizeof(int32_t) * e);
   L.scratch = off;
   off += al256(sizeof(int32_t) * (size_t)transpose_scratch_ints(N, E));
-  L.part = off;              // the receiver pass's and the sender pass's in turn
-  off += al256(std::max(part_bytes(a, kRecv), part_bytes(a, kSend)));
+  L.recv_part = off;
+  off += al256(part_bytes(a, kRecv));
+  L.send_part = off;
+  off += al256(part_bytes(a, kSend));
   L.total = off;
   return L;
 }
@@ -986,6 +1222,8 @@ tp_status_t attn_inputs(tp_attn_t h, int64_t N, int64_t E, const int32_t* rowptr
   a = h->proto;
   if (!rowptr || !q || !k || !v || (E > 0 && !src)) return set_failure(TP_ERR_INVALID_ARG, "NULL input");
   if (ldq < a.dq || ldk < a.dq || ldv < a.dv) return set_failure(TP_ERR_INVALID_ARG, "a row stride is below the row's width");
+  if (ldq >= 1 << 30 || ldk >= 1 << 30 || ldv >= 1 << 30)
+    return set_failure(TP_ERR_UNSUPPORTED, "row strides must stay below 2^30 floats");
   if (bucket && a.K == 0) return set_failure(TP_ERR_INVALID_ARG, "buckets given to an attention without buckets");
   if (table && !bucket && E > 0) return set_failure(TP_ERR_INVALID_ARG, "table needs bucket");
   if (table && a.K == 0) return set_failure(TP_ERR_INVALID_ARG, "table given to an attention without buckets");
@@ -1004,9 +1242,9 @@ tp_status_t attn_inputs(tp_attn_t h, int64_t N, int64_t E, const int32_t* rowptr
   a.q = q;
   a.k = k;
   a.v = v;
-  a.ldq = ldq;
-  a.ldk = ldk;
-  a.ldv = ldv;
+  a.ldq = (uint32_t)(ldq * 4);
+  a.ldk = (uint32_t)(ldk * 4);
+  a.ldv = (uint32_t)(ldv * 4);
   a.table = table;
   a.scale = scale;
   window_plan(a);
@@ -1014,7 +1252,7 @@ tp_status_t attn_inputs(tp_attn_t h, int64_t N, int64_t E, const int32_t* rowptr
 }
 
 bool rows4(const AttnArgs& a) {
-  return al16(a.q) && al16(a.k) && al16(a.v) && a.ldq % 4 == 0 && a.ldk % 4 == 0 && a.ldv % 4 == 0;
+  return al16(a.q) && al16(a.k) && al16(a.v) && a.ldq % 16 == 0 && a.ldk % 16 == 0 && a.ldv % 16 == 0;
 }
 
 bool head_map(const std::vector<IrrepTerm>& t, int heads, HeadMap& m, int& dim) {
@@ -1121,8 +1359,10 @@ tp_status_t tp_attn_fwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
     return set_failure(TP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   a.y = y;
   a.lse = lse;
-  return cuda_status(launch_pass(kFwd, a, attn->vec4 && rows4(a) && al16(y), static_cast<float*>(ws), reinterpret_cast<cudaStream_t>(stream)),
-                     "tp_attn_fwd");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_pass(kFwd, a, attn->vec4 && rows4(a) && al16(y), static_cast<float*>(ws), s);
+  if (e == cudaSuccess && a.n_win > 0) e = launch_after(k_attn_fwd_join, (unsigned)a.n_win, kJoinThreads, 0, s, a);
+  return cuda_status(e, "tp_attn_fwd");
 }
 
 tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* rowptr, const int32_t* src,
@@ -1188,24 +1428,38 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   a.hist = reinterpret_cast<float*>(w + L.hist);
   const bool vec4 = attn->vec4 && rows4(a) && al16(y) && al16(gy) && al16(gq) && al16(gk) && al16(gv) &&
                     (!gq || ldgq % 4 == 0) && (!gk || ldgk % 4 == 0) && (!gv || ldgv % 4 == 0);
-  float* part = reinterpret_cast<float*>(w + L.part);
-  e = launch_pass(kRecv, a, vec4, part, s);
-  if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, part, s);
-  if (e == cudaSuccess && gtable && E > 0) {
-    hist_plan(a);
-    const size_t smem = sizeof(float) * (size_t)a.K * a.H * a.hist_copies;
+  Tail tail{};
+  tail.recv_part = reinterpret_cast<float*>(w + L.recv_part);
+  tail.send_part = reinterpret_cast<float*>(w + L.send_part);
+  tail.recv_len = part_len(a, kRecv);
+  tail.send_len = part_len(a, kSend);
+  tail.recv_joins = gq ? a.n_win : 0;
+  tail.send_joins = send ? a.n_win : 0;
+  AttnArgs hist = a;
+  hist.hist_ctas = 0;
+  if (gtable && E > 0) hist_plan(hist);
+  // the table's CTAs run behind the sender pass's where their shared memory leaves those their place
+  const bool fused = send && hist.hist_ctas > 0 && hist_bytes(hist) <= 32 * 1024;
+  a.hist_ctas = fused ? hist.hist_ctas : 0;
+  a.hist_copies = hist.hist_copies;
+  a.hist_lanes = hist.hist_lanes;
+  e = launch_pass(kRecv, a, vec4, tail.recv_part, s);
+  if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, tail.send_part, s);
+  if (e == cudaSuccess && hist.hist_ctas > 0 && !fused) {
+    const size_t smem = hist_bytes(hist);
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_attn_table, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // an ordinary launch: set up early, its few CTAs would gather on the SMs that the receiver pass leaves
+    // first and run there one after another (162,892 edges: 46 instead of 16 us)
     if (e == cudaSuccess) {
-      k_attn_table<<<a.hist_ctas, kAttnThreads, smem, s>>>(a);
-      count_launches(1);
-      e = cudaGetLastError();
-    }
-    if (e == cudaSuccess && a.hist_ctas > 1) {
-      k_attn_table_sum<<<(a.K * a.H + 3) / 4, 128, 0, s>>>(a);
+      k_attn_table<<<hist.hist_ctas, kAttnThreads, smem, s>>>(hist);
       count_launches(1);
       e = cudaGetLastError();
     }
   }
+  a.hist_ctas = hist.hist_ctas;
+  const int sums = hist.hist_ctas > 1 ? (a.K * a.H + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
+  const unsigned rest = (unsigned)(tail.recv_joins + tail.send_joins + sums);
+  if (e == cudaSuccess && rest > 0) e = launch_after(k_attn_bwd_tail, rest, kJoinThreads, 0, s, a, tail);
   return cuda_status(e, "tp_attn_bwd");
 }
 
