@@ -1015,6 +1015,19 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_bwd_tail(const __grid_con
 // Distance buckets: squares in 64 bits (products of 32-bit floats are exact there), binary search.
 constexpr int kMaxBounds = 1023;
 
+__device__ __forceinline__ int bucket_of(float x, float y, float z, int n, const double* b2, double cut2) {
+  const double d2 = (double)x * x + (double)y * y + (double)z * z;
+  int lo = 0, hi = n;                    // the first bound above the distance lies in [lo, hi]
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (d2 >= b2[mid]) lo = mid + 1;
+    else hi = mid;
+  }
+  return d2 < cut2 ? lo : -1;
+}
+
+// QUAD: four edges a thread, whose 12 floats are three 16-byte reads; otherwise one.
+template <bool QUAD>
 __global__ void __launch_bounds__(256) k_buckets(int64_t E, const float* __restrict__ vec, int n, const float* __restrict__ bounds,
                                                  double cut2, int32_t* __restrict__ bucket) {
   __shared__ double b2[kMaxBounds + 1];
@@ -1023,17 +1036,18 @@ __global__ void __launch_bounds__(256) k_buckets(int64_t E, const float* __restr
     b2[i] = b < 0.0 ? -1.0 : b * b;
   }
   __syncthreads();
-  for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < E; e += (int64_t)gridDim.x * 256) {
-    const double x = vec[3 * e], y = vec[3 * e + 1], z = vec[3 * e + 2];
-    const double d2 = x * x + y * y + z * z;
-    int lo = 0, hi = n;                  // the first bound above the distance lies in [lo, hi]
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (d2 >= b2[mid]) lo = mid + 1;
-      else hi = mid;
+  const int64_t thread = blockIdx.x * (int64_t)256 + threadIdx.x, threads = (int64_t)gridDim.x * 256;
+  if constexpr (QUAD) {
+    const float4* v4 = reinterpret_cast<const float4*>(vec);
+    for (int64_t i = thread; i < E / 4; i += threads) {
+      const float4 p = __ldg(v4 + 3 * i), q = __ldg(v4 + 3 * i + 1), r = __ldg(v4 + 3 * i + 2);
+      reinterpret_cast<int4*>(bucket)[i] =
+          make_int4(bucket_of(p.x, p.y, p.z, n, b2, cut2), bucket_of(p.w, q.x, q.y, n, b2, cut2),
+                    bucket_of(q.z, q.w, r.x, n, b2, cut2), bucket_of(r.y, r.z, r.w, n, b2, cut2));
     }
-    bucket[e] = d2 < cut2 ? lo : -1;
   }
+  for (int64_t e = (QUAD ? E / 4 * 4 : 0) + thread; e < E; e += threads)
+    bucket[e] = bucket_of(vec[3 * e], vec[3 * e + 1], vec[3 * e + 2], n, b2, cut2);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -1472,9 +1486,14 @@ tp_status_t tp_distance_buckets(int64_t E, const float* vec, int32_t n_bounds, c
   if (E >= (int64_t)1 << 40) return set_failure(TP_ERR_UNSUPPORTED, "E too large");
   if (!vec || !bucket || (n_bounds > 0 && !bounds)) return set_failure(TP_ERR_INVALID_ARG, "NULL input or output");
   if (!al4(vec) || !al4(bounds) || !al4(bucket)) return set_failure(TP_ERR_INVALID_ARG, "pointers must be 4-byte aligned");
-  const int64_t grid = std::min<int64_t>((E + 255) / 256, 148 * 8);
-  k_buckets<<<(unsigned)grid, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(E, vec, n_bounds, bounds,
-                                                                              (double)cutoff * (double)cutoff, bucket);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const double cut2 = (double)cutoff * (double)cutoff;
+  // four edges a thread only where that still fills the SMs
+  const bool quad = al16(vec) && al16(bucket) && E >= 4 * 256 * 148;
+  const int64_t per = quad ? 1024 : 256;
+  const unsigned grid = (unsigned)std::min<int64_t>((E + per - 1) / per, 148 * 8);
+  if (quad) k_buckets<true><<<grid, 256, 0, s>>>(E, vec, n_bounds, bounds, cut2, bucket);
+  else k_buckets<false><<<grid, 256, 0, s>>>(E, vec, n_bounds, bounds, cut2, bucket);
   count_launches(1);
   return cuda_status(cudaGetLastError(), "tp_distance_buckets");
 }
