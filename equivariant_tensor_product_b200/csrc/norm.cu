@@ -1,17 +1,21 @@
 // Layer normalisation and channel dropout of irreps rows (include/tp_block.h).
 //
-// Norm.  A row is read once and kept in registers: its chunks of V floats (4, or 1 where a block's
-// length or a pointer does not allow 16 bytes) are dealt to a group of G lanes, S chunks a lane --
-// several rows a warp for narrow rows, a warp a row up to 9 chunks a lane, a CTA a row beyond.  A
-// chunk lies in one block, so a block's sum is the lanes' sums over their chunks of that block,
-// joined by shuffles: mean first, then the square of what is left of it, both in two reads of
-// registers instead of one pass with a difference of large sums.  Bound by the bytes (8 a float
-// forward, 12 backward).  The backward pass keeps every lane's sums of gy n and gy in registers over
-// all rows of the lane, adds them up per CTA, and a second kernel adds the CTAs, so gweight and
+// Norm.  The blocks of a row are independent, so each is a short row of its own: a CTA works on one
+// block of many rows.  A block's floats are read once and kept in registers: its chunks of V floats
+// (4, or 1 where a length or a pointer does not allow 16 bytes) are dealt to a group of G lanes, S
+// chunks a lane, several rows a warp where they are few.  A sum over the block is log2 G shuffles;
+// mean first, then the square of what is left of it, both from registers instead of one pass with a
+// difference of large sums.  The backward pass keeps every lane's sums of gy n and gy in registers
+// over all rows of the lane, adds them up per CTA, and a second kernel adds the CTAs, so gweight and
 // gbias cost no extra read of a row and have a fixed order.
 //
-// Rows that fit neither form (more than 2,048 chunks) take one CTA per row with three reads of the
-// row, the later ones from L1: k_norm_any.
+// Bound by the bytes (8 a float forward, 12 backward) as long as the instructions keep up, which is
+// why a block and not a row is the unit: with whole rows a warp (9 chunks a lane at 1,152 floats) the
+// sums over three blocks, each chunk asking which one it belongs to, took 365 us for 100,000 rows
+// backward, and with whole rows a CTA, through shared memory, 886 us.
+//
+// Blocks of more than 1,152 floats take one CTA per row with three reads of the row, the later ones
+// from L1: k_norm_any.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -30,7 +34,6 @@ namespace {
 constexpr int kNormMaxBlocks = 16;
 constexpr int kNormMaxDim = 8192;
 constexpr int kNormThreads = 128;
-constexpr int kNormMaxCtas = 148 * 2;
 
 struct NormArgs {
   int64_t N;
@@ -38,6 +41,9 @@ struct NormArgs {
   int off[kNormMaxBlocks], mul[kNormMaxBlocks], d[kNormMaxBlocks];
   int woff[kNormMaxBlocks];     // first weight
   int boff[kNormMaxBlocks];     // first bias, or -1 for a block without a mean
+  float inv[kNormMaxBlocks];    // 1 / floats of the block
+  int G[kNormMaxBlocks], S[kNormMaxBlocks];     // lanes of a row, chunks a lane
+  int cta0[kNormMaxBlocks + 1];                 // first CTA of the block
   float eps;
   const float* x;
   const float* weight;
@@ -47,9 +53,9 @@ struct NormArgs {
   float* gx;
   float* gweight;
   float* gbias;
-  float* part;                  // [ctas][2][dim]: sums over a CTA's rows of gy n and of gy
-  int ctas;
-  int G;                        // lanes of a row (one CTA a row: all its threads)
+  // sums over a CTA's rows of gy n and of gy: for each block [its CTAs][2][its floats], from part_at on
+  float* part;
+  int64_t part_at[kNormMaxBlocks];
 };
 
 constexpr int kRowThreads = 256;
@@ -82,235 +88,245 @@ __device__ __forceinline__ void write_chunk(float* p, const Chunk<V>& r) {
   else *p = r.x[0];
 }
 
-// The lanes of a row and the block of each of a lane's chunks.
-template <int V, int S, bool CTA>
-struct RowLanes {
-  int G, gl, bid[S];
-  float* red;                // CTA: [2][kRowThreads / 32], used in turn
-  int turn;
-
-  __device__ __forceinline__ RowLanes(const NormArgs& a, float* shared) : red(shared), turn(0) {
-    G = CTA ? kRowThreads : a.G;
-    gl = CTA ? threadIdx.x : threadIdx.x & (a.G - 1);
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const int at = offset(s);
-      int b = a.nb - 1;
-      while (b > 0 && at < a.off[b]) --b;
-      bid[s] = at < a.dim ? b : -1;
-    }
-  }
-  __device__ __forceinline__ int offset(int s) const { return (s * G + gl) * V; }
-  __device__ __forceinline__ float sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (CTA || G > o) v += __shfl_xor_sync(kFull, v, o);
-    if constexpr (CTA) {
-      float* r = red + turn * (kRowThreads / 32);
-      turn ^= 1;
-      if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
-      __syncthreads();
-      v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kRowThreads / 32; ++w) v += r[w];
-    }
-    return v;
-  }
-  // x becomes n = (x - mu) rho; rho of each chunk's block.
-  __device__ __forceinline__ void normalise(const NormArgs& a, Chunk<V> (&x)[S], float (&rho)[S]) {
-    for (int b = 0; b < a.nb; ++b) {
-      const float inv = 1.0f / (float)(a.mul[b] * a.d[b]);
-      float t = 0.0f;
-      if (a.boff[b] >= 0) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) t += bid[s] == b ? x[s].x[i] : 0.0f;
-        const float mu = sum(t) * inv;
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[s].x[i] -= bid[s] == b ? mu : 0.0f;
-      }
-      t = 0.0f;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        float q = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) q = fmaf(x[s].x[i], x[s].x[i], q);
-        t += bid[s] == b ? q : 0.0f;
-      }
-      const float r = rsqrtf(fmaf(sum(t), inv, a.eps));
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (bid[s] == b) rho[s] = r;
-    }
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[s].x[i] *= rho[s];
-  }
-};
-
-// Weight and bias of every float of a row, in shared memory (a chunk of a block with l > 0 covers parts of
-// several channels).
-__device__ __forceinline__ void expand_affine(const NormArgs& a, float* w, float* c) {
-  for (int i = threadIdx.x; i < a.dim; i += kRowThreads) {
-    int b = a.nb - 1;
-    while (b > 0 && i < a.off[b]) --b;
-    const int u = (i - a.off[b]) / a.d[b];
+// Weight and bias of every float of block b, in shared memory (a chunk of a block with l > 0 covers parts
+// of several channels).
+__device__ __forceinline__ void expand_affine(const NormArgs& a, int b, float* w, float* c) {
+  const int d = a.d[b], len = a.mul[b] * d;
+  for (int i = threadIdx.x; i < len; i += kRowThreads) {
+    const int u = i / d;
     w[i] = a.weight ? a.weight[a.woff[b] + u] : 1.0f;
     if (c) c[i] = a.bias && a.boff[b] >= 0 ? a.bias[a.boff[b] + u] : 0.0f;
   }
   __syncthreads();
 }
 
-template <int V, int S, int R, bool CTA>
-__global__ void __launch_bounds__(kRowThreads) k_norm_fwd(const __grid_constant__ NormArgs a) {
-  extern __shared__ __align__(16) float affine[];
-  __shared__ float red[2 * (kRowThreads / 32)];
-  float *w = affine, *c = affine + a.dim;
-  expand_affine(a, w, c);
-  RowLanes<V, S, CTA> L(a, red);
-  const int per = CTA ? 1 : kRowThreads / L.G, mine = CTA ? 0 : threadIdx.x / L.G;
-  for (int64_t n0 = (int64_t)blockIdx.x * per * R; n0 < a.N; n0 += (int64_t)gridDim.x * per * R) {
-    Chunk<V> x[R][S];
+// The lanes of a group and their chunks.
+template <int V, int S>
+struct RowLanes {
+  int G, gl, len;
+  float inv, eps;
+  bool mean;
+
+  __device__ __forceinline__ RowLanes(const NormArgs& a, int b) {
+    G = a.G[b];
+    gl = threadIdx.x & (G - 1);
+    len = a.mul[b] * a.d[b];
+    inv = a.inv[b];
+    eps = a.eps;
+    mean = a.boff[b] >= 0;
+  }
+  __device__ __forceinline__ int offset(int s) const { return (s * G + gl) * V; }
+  __device__ __forceinline__ bool has(int s) const { return offset(s) < len; }
+  __device__ __forceinline__ float sum(float v) const {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t n = n0 + (int64_t)r * per + mine;
+    for (int o = 16; o > 0; o >>= 1)
+      if (G > o) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  }
+  // x becomes n = (x - mu) rho; returns rho.  Chunks that the lane lacks stay 0.
+  __device__ __forceinline__ float normalise(Chunk<V> (&x)[S]) const {
+    float t = 0.0f;
+    if (mean) {
 #pragma unroll
-      for (int s = 0; s < S; ++s) x[r][s] = read_chunk<V>(a.x + n * a.dim + L.offset(s), n < a.N && L.bid[s] >= 0);
-    }
+      for (int s = 0; s < S; ++s)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t n = n0 + (int64_t)r * per + mine;
-      float rho[S] = {};
-      L.normalise(a, x[r], rho);
+        for (int i = 0; i < V; ++i) t += x[s].x[i];
+      const float mu = sum(t) * inv;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        if (n >= a.N || L.bid[s] < 0) continue;
+        const float m = has(s) ? mu : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[s].x[i] -= m;
+      }
+      t = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < V; ++i) t = fmaf(x[s].x[i], x[s].x[i], t);
+    const float rho = rsqrtf(fmaf(sum(t), inv, eps));
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[s].x[i] *= rho;
+    return rho;
+  }
+};
+
+// Rows in flight a group: about four chunks (V = 4) or eight floats a lane on their way.
+template <int V, int S>
+struct RowsAtOnce {
+  static constexpr int value = V == 4 ? (S == 1 ? 4 : S == 2 ? 2 : 1) : (S <= 2 ? 4 : S <= 4 ? 2 : 1);
+};
+
+template <int V, int S>
+__device__ __forceinline__ void norm_fwd_block(const NormArgs& a, int b, float* affine) {
+  constexpr int R = RowsAtOnce<V, S>::value;
+  const RowLanes<V, S> L(a, b);
+  float *w = affine, *c = affine + L.len;
+  expand_affine(a, b, w, c);
+  const int per = kRowThreads / L.G, mine = threadIdx.x / L.G, cta = blockIdx.x - a.cta0[b], ctas = a.cta0[b + 1] - a.cta0[b];
+  const int64_t hop = (int64_t)per * a.dim;
+  for (int64_t n0 = (int64_t)cta * per * R + mine; n0 - mine < a.N; n0 += (int64_t)ctas * per * R) {
+    Chunk<V> x[R][S];
+    const float* xp = a.x + n0 * a.dim + a.off[b];
+    float* yp = a.y + n0 * a.dim + a.off[b];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int s = 0; s < S; ++s) x[r][s] = read_chunk<V>(xp + r * hop + L.offset(s), n0 + r * per < a.N && L.has(s));
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      L.normalise(x[r]);
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (n0 + r * per >= a.N || !L.has(s)) continue;
         const Chunk<V> ws = read_chunk<V>(w + L.offset(s), true), cs = read_chunk<V>(c + L.offset(s), true);
         Chunk<V> y;
 #pragma unroll
         for (int i = 0; i < V; ++i) y.x[i] = fmaf(x[r][s].x[i], ws.x[i], cs.x[i]);
-        write_chunk<V>(a.y + n * a.dim + L.offset(s), y);
+        write_chunk<V>(yp + r * hop + L.offset(s), y);
       }
     }
   }
 }
 
-template <int V, int S, int R, bool CTA>
-__global__ void __launch_bounds__(kRowThreads) k_norm_bwd(const __grid_constant__ NormArgs a) {
-  extern __shared__ __align__(16) float affine[];
-  __shared__ float red[2 * (kRowThreads / 32)];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  float* w = affine;
-  expand_affine(a, w, nullptr);
-  RowLanes<V, S, CTA> L(a, red);
-  const int per = CTA ? 1 : kRowThreads / L.G, mine = CTA ? 0 : threadIdx.x / L.G;
+// MEAN: a 0e block.
+template <int V, int S, bool MEAN>
+__device__ __forceinline__ void norm_bwd_block(const NormArgs& a, int b, float* affine) {
+  constexpr int R = RowsAtOnce<V, S>::value;
+  const RowLanes<V, S> L(a, b);
+  expand_affine(a, b, affine, nullptr);
+  const int per = kRowThreads / L.G, mine = threadIdx.x / L.G, cta = blockIdx.x - a.cta0[b], ctas = a.cta0[b + 1] - a.cta0[b];
+  const int64_t hop = (int64_t)per * a.dim;
   Chunk<V> sw[S], sb[S];
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int i = 0; i < V; ++i) sw[s].x[i] = sb[s].x[i] = 0.0f;
-  for (int64_t n0 = (int64_t)blockIdx.x * per * R; n0 < a.N; n0 += (int64_t)gridDim.x * per * R) {
+  for (int64_t n0 = (int64_t)cta * per * R + mine; n0 - mine < a.N; n0 += (int64_t)ctas * per * R) {
     Chunk<V> x[R][S], g[R][S];
+    const int64_t at = n0 * a.dim + a.off[b];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t n = n0 + (int64_t)r * per + mine;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        const bool on = n < a.N && L.bid[s] >= 0;
-        x[r][s] = read_chunk<V>(a.x + n * a.dim + L.offset(s), on);
-        g[r][s] = read_chunk<V>(a.gy + n * a.dim + L.offset(s), on);
+        const bool on = n0 + r * per < a.N && L.has(s);
+        x[r][s] = read_chunk<V>(a.x + at + r * hop + L.offset(s), on);
+        g[r][s] = read_chunk<V>(a.gy + at + r * hop + L.offset(s), on);
       }
-    }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t n = n0 + (int64_t)r * per + mine;
-      float rho[S] = {};
-      L.normalise(a, x[r], rho);
+      const float rho = L.normalise(x[r]);
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          sw[s].x[i] = fmaf(g[r][s].x[i], x[r][s].x[i], sw[s].x[i]);
-          sb[s].x[i] += g[r][s].x[i];
-        }
-      if (!a.gx) continue;
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const Chunk<V> ws = read_chunk<V>(w + L.offset(s), L.bid[s] >= 0);
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[r][s].x[i] *= ws.x[i];
-      }
-      float s1[S] = {}, s2[S] = {};
-      for (int b = 0; b < a.nb; ++b) {
-        const float inv = 1.0f / (float)(a.mul[b] * a.d[b]);
-        float t1 = 0.0f, t2 = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          float u1 = 0.0f, u2 = 0.0f;
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            u1 += g[r][s].x[i];
-            u2 = fmaf(g[r][s].x[i], x[r][s].x[i], u2);
-          }
-          t1 += L.bid[s] == b ? u1 : 0.0f;
-          t2 += L.bid[s] == b ? u2 : 0.0f;
-        }
-        t1 = a.boff[b] >= 0 ? L.sum(t1) * inv : 0.0f;
-        t2 = L.sum(t2) * inv;
+        for (int i = 0; i < V; ++i) sw[s].x[i] = fmaf(g[r][s].x[i], x[r][s].x[i], sw[s].x[i]);
+      if constexpr (MEAN) {
 #pragma unroll
         for (int s = 0; s < S; ++s)
-          if (L.bid[s] == b) {
-            s1[s] = t1;
-            s2[s] = t2;
-          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) sb[s].x[i] += g[r][s].x[i];
       }
+      if (!a.gx) continue;
+      float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        if (n >= a.N || L.bid[s] < 0) continue;
+        const Chunk<V> ws = read_chunk<V>(affine + L.offset(s), L.has(s));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          g[r][s].x[i] *= ws.x[i];
+          t1 += g[r][s].x[i];
+          t2 = fmaf(g[r][s].x[i], x[r][s].x[i], t2);
+        }
+      }
+      t1 = MEAN ? L.sum(t1) * L.inv : 0.0f;
+      t2 = L.sum(t2) * L.inv;
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        if (n0 + r * per >= a.N || !L.has(s)) continue;
         Chunk<V> gx;
 #pragma unroll
-        for (int i = 0; i < V; ++i) gx.x[i] = rho[s] * (g[r][s].x[i] - s1[s] - x[r][s].x[i] * s2[s]);
-        write_chunk<V>(a.gx + n * a.dim + L.offset(s), gx);
+        for (int i = 0; i < V; ++i) gx.x[i] = rho * (g[r][s].x[i] - t1 - x[r][s].x[i] * t2);
+        write_chunk<V>(a.gx + at + r * hop + L.offset(s), gx);
       }
     }
   }
   if (!a.part) return;
-  // the CTA's sums: lanes of a warp that hold the same chunks, then warp after warp
-  float* total = affine;
+  // the CTA's sums: lanes of a warp that hold the same chunks by shuffles, then the warps in order
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.dim; i += kRowThreads) total[i] = 0.0f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* sums = affine + warp * 2 * L.len;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (!CTA && o >= L.G) {
+    if (o >= L.G) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           sw[s].x[i] += __shfl_xor_sync(kFull, sw[s].x[i], o);
-          sb[s].x[i] += __shfl_xor_sync(kFull, sb[s].x[i], o);
+          if constexpr (MEAN) sb[s].x[i] += __shfl_xor_sync(kFull, sb[s].x[i], o);
         }
     }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int turn = 0; turn < (CTA ? 1 : kRowThreads / 32); ++turn) {
-    if (CTA || (warp == turn && lane < L.G)) {
+  if (lane < L.G) {
 #pragma unroll
-      for (int s = 0; s < S; ++s)
-        if (L.bid[s] >= 0) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            total[L.offset(s) + i] += sw[s].x[i];
-            total[a.dim + L.offset(s) + i] += sb[s].x[i];
-          }
-        }
-    }
-    __syncthreads();
+    for (int s = 0; s < S; ++s)
+      if (L.has(s)) {
+        write_chunk<V>(sums + L.offset(s), sw[s]);
+        if constexpr (MEAN) write_chunk<V>(sums + L.len + L.offset(s), sb[s]);
+      }
   }
-  for (int i = threadIdx.x; i < 2 * a.dim; i += kRowThreads) a.part[(int64_t)blockIdx.x * 2 * a.dim + i] = total[i];
+  __syncthreads();
+  float* out = a.part + a.part_at[b] + (int64_t)cta * 2 * L.len;
+  for (int i = threadIdx.x; i < (MEAN ? 2 : 1) * L.len; i += kRowThreads) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowThreads / 32; ++w) t += affine[w * 2 * L.len + i];
+    out[i] = t;
+  }
+}
+
+// CTAs a SM that the registers are held to: a lane keeps three to four arrays of its chunks backward.
+__host__ __device__ constexpr int ctas_per_sm(bool bwd, int floats) {
+  return bwd ? (floats <= 4 ? 4 : floats <= 8 ? 3 : floats <= 24 ? 2 : 1) : (floats <= 16 ? 4 : floats <= 24 ? 3 : 2);
+}
+
+// MOST: the most chunks a lane of any block, which sets the registers; each block runs with its own.
+template <bool BWD, int V, int MOST>
+__global__ void __launch_bounds__(kRowThreads, ctas_per_sm(BWD, V * MOST)) k_norm(const __grid_constant__ NormArgs a) {
+  extern __shared__ __align__(16) float affine[];
+  if (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int b = 0;
+  while ((int)blockIdx.x >= a.cta0[b + 1]) ++b;
+#define TP_NORM_CASE(n)                                                          \
+  case n:                                                                        \
+    if constexpr (n <= MOST) {                                                   \
+      if constexpr (!BWD) norm_fwd_block<V, n>(a, b, affine);                    \
+      else if (a.boff[b] >= 0) norm_bwd_block<V, n, true>(a, b, affine);         \
+      else norm_bwd_block<V, n, false>(a, b, affine);                            \
+    }                                                                            \
+    break;
+  if constexpr (V == 4) {
+    switch (a.S[b]) {
+      TP_NORM_CASE(1)
+      TP_NORM_CASE(2)
+      TP_NORM_CASE(3)
+      TP_NORM_CASE(4)
+      TP_NORM_CASE(6)
+      TP_NORM_CASE(9)
+    }
+  } else {
+    switch (a.S[b]) {
+      TP_NORM_CASE(1)
+      TP_NORM_CASE(2)
+      TP_NORM_CASE(4)
+      TP_NORM_CASE(8)
+      TP_NORM_CASE(16)
+      TP_NORM_CASE(24)
+      TP_NORM_CASE(36)
+    }
+  }
+#undef TP_NORM_CASE
 }
 
 // Sum over the CTA, the same value in every thread.  Two barriers: s is free again afterwards.
@@ -388,16 +404,25 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_any(const __grid_constant
   }
   __syncthreads();
   if (sums)
-    for (int i = tid; i < 2 * a.dim; i += kNormThreads) a.part[(int64_t)blockIdx.x * 2 * a.dim + i] = acc[i];
+    for (int b = 0; b < a.nb; ++b) {
+      const int len = a.mul[b] * a.d[b];
+      float* out = a.part + a.part_at[b] + (int64_t)blockIdx.x * 2 * len;
+      for (int i = tid; i < len; i += kNormThreads) {
+        out[i] = acc[a.off[b] + i];
+        out[len + i] = acc[a.dim + a.off[b] + i];
+      }
+    }
 }
 
-// gweight[u] = sum over CTAs and m, gbias[u] = sum over CTAs, in fixed orders.  One CTA for 32 channels of
-// a block: its warps take every 16th CTA's partials, whose floats they read side by side; 64-bit sums,
-// the partials being up to a few hundred terms of both signs.
+// gweight[u] = sum over CTAs and m, gbias[u] = sum over CTAs, in fixed orders.  One CTA for the channels
+// that 32 floats of a block hold (32, 10, 6 or 4), a lane a float; its 16 warps take every 16th CTA's
+// partials, eight reads in flight each; 64-bit sums, the partials being up to some hundred terms of both
+// signs.  With 32 channels a CTA, four CTAs had all the reads of a small row's norm: 14 us for 1,536 rows
+// of 288 floats.
 constexpr int kSumThreads = 512;
 
 __global__ void __launch_bounds__(kSumThreads) k_norm_sums(const __grid_constant__ NormArgs a) {
-  __shared__ double sums[kSumThreads / 32][7 * 32];
+  __shared__ double sums[kSumThreads / 32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int tile = blockIdx.x, b = 0;
   bool bias = false;
@@ -407,29 +432,24 @@ __global__ void __launch_bounds__(kSumThreads) k_norm_sums(const __grid_constant
       b = 0;
     }
     if (bias && a.boff[b] < 0) continue;
-    const int tiles = (a.mul[b] + 31) / 32;
+    const int wide = 32 / a.d[b], tiles = (a.mul[b] + wide - 1) / wide;
     if (tile < tiles) break;
     tile -= tiles;
   }
-  const int d = bias ? 1 : a.d[b], u0 = tile * 32, channels = min(32, a.mul[b] - u0);
-  const float* p = a.part + (bias ? a.dim : 0) + a.off[b] + u0 * d;
-  double t[7] = {};
+  const int d = a.d[b], wide = 32 / d, u0 = tile * wide, channels = min(wide, a.mul[b] - u0);
+  const int len = a.mul[b] * d, ctas = a.cta0[b + 1] - a.cta0[b];
+  const float* p = a.part + a.part_at[b] + (bias ? len : 0) + u0 * d + min(lane, channels * d - 1);
+  double t = 0.0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-#pragma unroll 4
-  for (int c = warp; c < a.ctas; c += kSumThreads / 32) {
-#pragma unroll
-    for (int m = 0; m < 7; ++m) {
-      const int i = m * 32 + lane;
-      if (m < d && i < channels * d) t[m] += (double)p[(int64_t)c * 2 * a.dim + i];
-    }
-  }
-#pragma unroll
-  for (int m = 0; m < 7; ++m) sums[warp][m * 32 + lane] = t[m];
+#pragma unroll 8
+  for (int c = warp; c < ctas; c += kSumThreads / 32) t += (double)p[(int64_t)c * 2 * len];
+  sums[warp][lane] = t;
   __syncthreads();
   float* out = bias ? a.gbias : a.gweight;
   if (threadIdx.x < channels && out) {
     double v = 0.0;
     for (int m = 0; m < d; ++m)
+#pragma unroll
       for (int w = 0; w < kSumThreads / 32; ++w) v += sums[w][threadIdx.x * d + m];
     out[(bias ? a.boff[b] : a.woff[b]) + u0 + threadIdx.x] = (float)v;
   }
@@ -520,68 +540,105 @@ tp_status_t parse_rows(const char* irreps, std::vector<IrrepTerm>& t, int& dim) 
   return TP_OK;
 }
 
-// How a row is spread: lanes G, chunks a lane S (0: neither form takes it), one CTA a row.
-struct RowForm {
-  int G, S;
-  bool cta;
-};
-
-RowForm row_form(int dim, int V) {
-  const int chunks = dim / V;
-  if (chunks > 9 * 32) {
-    const int S = (chunks + kRowThreads - 1) / kRowThreads;
-    return RowForm{kRowThreads, S <= 2 ? 2 : S <= 4 ? 4 : S <= 8 ? 8 : 0, true};
+// Lanes and chunks a lane of each block: the fewest idle lanes among the forms with at most four chunks
+// (V = 4) or sixteen floats a lane, and of those with equally few the one with most lanes; a whole warp for
+// longer blocks.  Returns the most chunks a lane, 0 if a block is too long.
+int row_forms(NormArgs& a, int V) {
+  static const int slots4[] = {1, 2, 3, 4, 6, 9}, slots1[] = {1, 2, 4, 8, 16, 24, 36};
+  int most = 0;
+  for (int b = 0; b < a.nb; ++b) {
+    const int chunks = a.mul[b] * a.d[b] / V;
+    a.S[b] = 0;
+    for (int G = 32; G >= 1; G /= 2) {
+      int S = 0;
+      if (V == 4) {
+        for (int s : slots4)
+          if (S == 0 && s * G >= chunks) S = s;
+      } else {
+        for (int s : slots1)
+          if (S == 0 && s * G >= chunks) S = s;
+      }
+      if (S == 0 || (a.S[b] != 0 && (S > (V == 4 ? 4 : 16) || G * S >= a.G[b] * a.S[b]))) continue;
+      a.G[b] = G;
+      a.S[b] = S;
+    }
+    if (a.S[b] == 0) return 0;
+    most = std::max(most, a.S[b]);
   }
-  RowForm f{32, (chunks + 31) / 32, false};
-  // at most four chunks a lane where a row is narrow enough, with as few idle lanes as possible
-  for (int G = 16; G >= 1; G /= 2) {
-    const int S = (chunks + G - 1) / G;
-    if (S <= 4 && G * S < f.G * f.S) f = RowForm{G, S, false};
-  }
-  if (f.S > 4) f.S = f.S <= 6 ? 6 : 9;
-  return f;
+  return most;
 }
 
-template <bool BWD, int V, int S, int R, bool CTA>
-cudaError_t launch_rows(const NormArgs& a, unsigned grid, cudaStream_t s) {
-  const size_t smem = sizeof(float) * 2 * (size_t)a.dim;
-  auto kernel = BWD ? k_norm_bwd<V, S, R, CTA> : k_norm_fwd<V, S, R, CTA>;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// Shares `total` CTAs out among the blocks by their floats, at least one each and none without a row.
+// `any`: one row a CTA and every CTA on all blocks (k_norm_any).
+void share_ctas(NormArgs& a, int64_t N, int total, bool any) {
+  int64_t at = 0;
+  a.cta0[0] = 0;
+  for (int b = 0; b < a.nb; ++b) {
+    const int len = a.mul[b] * a.d[b];
+    int64_t n;
+    if (any) {
+      n = std::min<int64_t>(N, total);
+    } else {
+      const int per = kRowThreads / a.G[b];
+      n = std::min<int64_t>((N + per - 1) / per, ((int64_t)total * len + a.dim - 1) / a.dim);
+    }
+    n = std::max<int64_t>(n, 1);
+    a.cta0[b + 1] = a.cta0[b] + (int)n;
+    a.part_at[b] = at;
+    at += n * 2 * len;
+  }
+}
+
+// CTAs of the backward pass: what is resident at once, each leaves a partial of the weight gradients.
+int most_slots(int most, int V) {
+  if (V == 4) return most <= 1 ? 1 : most <= 2 ? 2 : most <= 4 ? 4 : most <= 6 ? 6 : 9;
+  return most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 36;
+}
+int bwd_ctas(const NormArgs& a, int most, int V) {
+  if (most == 0) return 148 * std::max(1, std::min(8, 160 * 1024 / (8 * a.dim)));
+  return 148 * ctas_per_sm(true, V * most_slots(most, V));
+}
+
+// Floats of the partials with either width of a chunk, so that the workspace does not depend on alignment.
+size_t part_floats(const NormArgs& proto, bool vec4, int64_t N) {
+  size_t n = 0;
+  for (int V : {1, 4}) {
+    if (V == 4 && !vec4) continue;
+    NormArgs a = proto;
+    const int most = row_forms(a, V);
+    share_ctas(a, N, bwd_ctas(a, most, V), most == 0);
+    const int b = a.nb - 1;
+    n = std::max(n, (size_t)a.part_at[b] + (size_t)(a.cta0[b + 1] - a.cta0[b]) * 2 * a.mul[b] * a.d[b]);
+  }
+  return n;
+}
+
+template <bool BWD, int V, int MOST>
+cudaError_t launch_most(const NormArgs& a, size_t smem, cudaStream_t s) {
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(k_norm<BWD, V, MOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, kRowThreads, smem, s>>>(a);
+  k_norm<BWD, V, MOST><<<a.cta0[a.nb], kRowThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-// Rows in flight a lane group: enough that a lane has at least four chunks on their way.
-constexpr int rows_at_once(int S) { return S == 1 ? 4 : S == 2 ? 2 : 1; }
-
-template <bool BWD, int V>
-cudaError_t launch_form(const NormArgs& a, const RowForm& f, unsigned grid, cudaStream_t s) {
-  if (f.cta) {
-    switch (f.S) {
-      case 2: return launch_rows<BWD, V, 2, 1, true>(a, grid, s);
-      case 4: return launch_rows<BWD, V, 4, 1, true>(a, grid, s);
-      default: return launch_rows<BWD, V, 8, 1, true>(a, grid, s);
-    }
+template <bool BWD>
+cudaError_t launch_norm(const NormArgs& a, int most, int V, cudaStream_t s) {
+  int len = 0;
+  for (int b = 0; b < a.nb; ++b) len = std::max(len, a.mul[b] * a.d[b]);
+  const size_t smem = sizeof(float) * 2 * (size_t)len * (BWD && a.part ? kRowThreads / 32 : 1);
+  switch (most_slots(most, V) * 8 + V) {
+    case 1 * 8 + 4: return launch_most<BWD, 4, 1>(a, smem, s);
+    case 2 * 8 + 4: return launch_most<BWD, 4, 2>(a, smem, s);
+    case 4 * 8 + 4: return launch_most<BWD, 4, 4>(a, smem, s);
+    case 6 * 8 + 4: return launch_most<BWD, 4, 6>(a, smem, s);
+    case 9 * 8 + 4: return launch_most<BWD, 4, 9>(a, smem, s);
+    case 4 * 8 + 1: return launch_most<BWD, 1, 4>(a, smem, s);
+    case 8 * 8 + 1: return launch_most<BWD, 1, 8>(a, smem, s);
+    case 16 * 8 + 1: return launch_most<BWD, 1, 16>(a, smem, s);
+    default: return launch_most<BWD, 1, 36>(a, smem, s);
   }
-  switch (f.S) {
-    case 1: return launch_rows<BWD, V, 1, rows_at_once(1), false>(a, grid, s);
-    case 2: return launch_rows<BWD, V, 2, rows_at_once(2), false>(a, grid, s);
-    case 3: return launch_rows<BWD, V, 3, rows_at_once(3), false>(a, grid, s);
-    case 4: return launch_rows<BWD, V, 4, rows_at_once(4), false>(a, grid, s);
-    case 6: return launch_rows<BWD, V, 6, rows_at_once(6), false>(a, grid, s);
-    default: return launch_rows<BWD, V, 9, rows_at_once(9), false>(a, grid, s);
-  }
-}
-
-// CTAs of the backward pass (each leaves a partial of the weight gradients): two a SM, and fewer where
-// a lane group would not have two rows.
-int norm_ctas(int64_t N, int dim) {
-  const RowForm f = row_form(dim, 1);
-  const int64_t per = f.cta || f.S == 0 ? 1 : kRowThreads / f.G;
-  return (int)std::max<int64_t>(1, std::min<int64_t>((N + 2 * per - 1) / (2 * per), kNormMaxCtas));
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -619,6 +676,7 @@ tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps) try 
     a.off[i] = off;
     a.mul[i] = b.mul;
     a.d[i] = 2 * b.l + 1;
+    a.inv[i] = 1.0f / (float)(a.mul[i] * a.d[i]);
     a.woff[i] = a.n_weights;
     a.boff[i] = -1;
     if (b.l == 0 && b.parity == 1) {
@@ -654,7 +712,7 @@ tp_status_t tp_norm_workspace_size(tp_norm_t norm, int64_t N, int32_t op, size_t
   if (!norm || !bytes) return set_failure(TP_ERR_INVALID_ARG, "NULL argument");
   if (N < 0) return set_failure(TP_ERR_INVALID_ARG, "N must be non-negative");
   if (op != TP_OP_FWD && op != TP_OP_BWD) return set_failure(TP_ERR_INVALID_ARG, "op must be TP_OP_FWD or TP_OP_BWD");
-  *bytes = op == TP_OP_FWD ? 0 : sizeof(float) * 2 * (size_t)norm->proto.dim * (size_t)norm_ctas(N, norm->proto.dim);
+  *bytes = op == TP_OP_FWD ? 0 : sizeof(float) * part_floats(norm->proto, norm->vec4, N);
   return TP_OK;
 }
 
@@ -674,17 +732,14 @@ tp_status_t tp_norm_fwd(tp_norm_t norm, int64_t N, const float* x, const float* 
   a.bias = bias;
   a.y = y;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int V = norm->vec4 && al16(x) && al16(y) ? 4 : 1;
-  const RowForm f = row_form(a.dim, V);
-  a.G = f.G;
+  const int V = norm->vec4 && al16(x) && al16(y) ? 4 : 1, most = row_forms(a, V);
   count_launches(1);
-  if (f.S == 0) {
+  if (most == 0) {
     k_norm_any<false><<<(unsigned)std::min<int64_t>(N, 148 * 16), kNormThreads, 0, s>>>(a);
     return cuda_status(cudaGetLastError(), "tp_norm_fwd");
   }
-  const int64_t per = (f.cta ? 1 : kRowThreads / f.G) * rows_at_once(f.cta ? 3 : f.S);
-  const unsigned grid = (unsigned)std::min<int64_t>((N + per - 1) / per, 148 * 8);
-  return cuda_status(V == 4 ? launch_form<false, 4>(a, f, grid, s) : launch_form<false, 1>(a, f, grid, s), "tp_norm_fwd");
+  share_ctas(a, N, 148 * 8, false);
+  return cuda_status(launch_norm<false>(a, most, V, s), "tp_norm_fwd");
 }
 
 tp_status_t tp_norm_bwd(tp_norm_t norm, int64_t N, const float* x, const float* weight, const float* gy, float* gx,
@@ -705,28 +760,29 @@ tp_status_t tp_norm_bwd(tp_norm_t norm, int64_t N, const float* x, const float* 
   a.gx = gx;
   a.gweight = gweight;
   a.gbias = gbias;
-  a.ctas = norm_ctas(N, a.dim);
-  const size_t need = sums ? sizeof(float) * 2 * (size_t)a.dim * (size_t)a.ctas : 0;
+  const size_t need = sums ? sizeof(float) * part_floats(a, norm->vec4, N) : 0;
   if (sums && (!ws || ws_bytes < need)) return set_failure(TP_ERR_WORKSPACE, "workspace too small");
   a.part = sums ? static_cast<float*>(ws) : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int V = norm->vec4 && al16(x) && al16(gy) && al16(gx) ? 4 : 1;
-  const RowForm f = row_form(a.dim, V);
-  a.G = f.G;
+  const int V = norm->vec4 && al16(x) && al16(gy) && al16(gx) ? 4 : 1, most = row_forms(a, V);
+  share_ctas(a, N, bwd_ctas(a, most, V), most == 0);
   cudaError_t e = cudaSuccess;
   count_launches(1);
-  if (f.S == 0) {
+  if (most == 0) {
     const int smem = sums ? (int)(sizeof(float) * 2 * a.dim) : 0;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_norm_any<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem > 40 * 1024) e = cudaFuncSetAttribute(k_norm_any<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return cuda_status(e, "tp_norm_bwd");
-    k_norm_any<true><<<a.ctas, kNormThreads, smem, s>>>(a);
+    k_norm_any<true><<<a.cta0[1], kNormThreads, smem, s>>>(a);
     e = cudaGetLastError();
   } else {
-    e = V == 4 ? launch_form<true, 4>(a, f, (unsigned)a.ctas, s) : launch_form<true, 1>(a, f, (unsigned)a.ctas, s);
+    e = launch_norm<true>(a, most, V, s);
   }
   if (e == cudaSuccess && sums) {
     unsigned tiles = 0;
-    for (int b = 0; b < a.nb; ++b) tiles += (unsigned)((a.mul[b] + 31) / 32) * (a.boff[b] >= 0 ? 2 : 1);
+    for (int b = 0; b < a.nb; ++b) {
+      const int wide = 32 / a.d[b];
+      tiles += (unsigned)((a.mul[b] + wide - 1) / wide) * (a.boff[b] >= 0 ? 2 : 1);
+    }
     cudaLaunchAttribute attr;            // set up while the first kernel runs; it waits for its end
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
