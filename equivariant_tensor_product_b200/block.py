@@ -9,7 +9,7 @@ from typing import Optional, Sequence
 import torch
 
 from ._lib import TP_OP_BWD, TP_OP_FWD, check, load
-from .attn import _on, _same_device, _shape, _workspace
+from ._marshal import device_index, f32, on, ptr, stream_of, workspace
 from .ops import _ptr, _stream
 
 __all__ = ["Linear", "Gate", "tp_linear_fwd", "tp_linear_bwd", "tp_linear_workspace_size", "tp_gate_fwd",
@@ -146,6 +146,7 @@ class Norm:
         vals = [C.c_int64() for _ in range(3)]
         check(lib.tp_norm_query(self.handle, *[C.byref(v) for v in vals]), "tp_norm_query")
         self.dim, self.n_weights, self.n_bias = (v.value for v in vals)
+        self._size = None       # (rows, workspace bytes) of the last backward call
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -160,47 +161,43 @@ def tp_norm_workspace_size(norm: Norm, N: int, op: int) -> int:
     return out.value
 
 
-def _norm_inputs(norm, x, weight, bias):
-    N, dev = x.shape[0], x.device
-    _shape(x, (N, norm.dim), "x")
-    _shape(weight, (norm.n_weights,), "weight")
-    _shape(bias, (norm.n_bias,), "bias")
-    _same_device(dev, weight=weight, bias=bias)
-    return N, dev
-
-
 def tp_norm_fwd(norm: Norm, x, weight=None, bias=None, y=None, stream=None):
     """y = norm(x); weight [n_weights] and bias [n_bias] default to ones and zeros.  y may be x."""
-    N, dev = _norm_inputs(norm, x, weight, bias)
-    _shape(y, (N, norm.dim), "y")
-    _same_device(dev, y=y)
-    with _on(dev, stream):
-        y = torch.empty(N, norm.dim, dtype=torch.float32, device=dev) if y is None else y
-        check(load().tp_norm_fwd(norm.handle, N, _ptr(x, torch.float32, "x"), _ptr(weight, torch.float32, "weight"),
-                                 _ptr(bias, torch.float32, "bias"), _ptr(y, torch.float32, "y"),
-                                 torch.cuda.current_stream(dev).cuda_stream), "tp_norm_fwd")
+    N = x.shape[0]
+    shape = (N, norm.dim)
+    if x.shape != shape:
+        raise ValueError(f"x must have shape {list(shape)}, got {list(x.shape)}")
+    if weight is not None and weight.shape != (norm.n_weights,):
+        raise ValueError(f"weight must have shape {[norm.n_weights]}, got {list(weight.shape)}")
+    i = device_index(x, "x")
+    with on(i, stream):
+        y = torch.empty(shape, dtype=torch.float32, device=x.device) if y is None else y
+        check(norm._lib.tp_norm_fwd(norm.handle, N, f32(x, i, shape, "x"), f32(weight, i, None, "weight"),
+                                    f32(bias, i, (norm.n_bias,), "bias"), f32(y, i, shape, "y"), stream_of(i)),
+              "tp_norm_fwd")
     return y
 
 
 def tp_norm_bwd(norm: Norm, x, gy, weight=None, need_gx=True, need_gweight=True, need_gbias=True, gx=None,
                 gweight=None, gbias=None, ws=None, stream=None):
     """(gx, gweight, gbias) against gy, each None when not requested.  gx may be gy."""
-    N, dev = _norm_inputs(norm, x, weight, None)
-    _same_device(dev, gy=gy, gx=gx, gweight=gweight, gbias=gbias, ws=ws)
-    for t, shape, name in ((gy, (N, norm.dim), "gy"), (gx, (N, norm.dim), "gx"),
-                           (gweight, (norm.n_weights,), "gweight"), (gbias, (norm.n_bias,), "gbias")):
-        _shape(t, shape, name)
-    with _on(dev, stream):
-        new = lambda *shape: torch.empty(*shape, dtype=torch.float32, device=dev)
-        gx = new(N, norm.dim) if gx is None and need_gx else gx
-        gweight = new(norm.n_weights) if gweight is None and need_gweight else gweight
-        gbias = new(norm.n_bias) if gbias is None and need_gbias else gbias
-        ws = _workspace(ws, tp_norm_workspace_size(norm, N, TP_OP_BWD), dev)
-        check(load().tp_norm_bwd(norm.handle, N, _ptr(x, torch.float32, "x"), _ptr(weight, torch.float32, "weight"),
-                                 _ptr(gy, torch.float32, "gy"), _ptr(gx, torch.float32, "gx"),
-                                 _ptr(gweight, torch.float32, "gweight"), _ptr(gbias, torch.float32, "gbias"),
-                                 ws.data_ptr(), ws.numel() * ws.element_size(),
-                                 torch.cuda.current_stream(dev).cuda_stream), "tp_norm_bwd")
+    N = x.shape[0]
+    shape = (N, norm.dim)
+    if x.shape != shape:
+        raise ValueError(f"x must have shape {list(shape)}, got {list(x.shape)}")
+    i = device_index(x, "x")
+    with on(i, stream):
+        dev = x.device
+        gx = torch.empty(shape, dtype=torch.float32, device=dev) if gx is None and need_gx else gx
+        gweight = torch.empty(norm.n_weights, dtype=torch.float32, device=dev) if gweight is None and need_gweight else gweight
+        gbias = torch.empty(norm.n_bias, dtype=torch.float32, device=dev) if gbias is None and need_gbias else gbias
+        if norm._size is None or norm._size[0] != N:
+            norm._size = (N, tp_norm_workspace_size(norm, N, TP_OP_BWD))
+        ws, ws_ptr, ws_bytes = workspace(ws, norm._size[1], i)
+        check(norm._lib.tp_norm_bwd(norm.handle, N, f32(x, i, shape, "x"), f32(weight, i, (norm.n_weights,), "weight"),
+                                    f32(gy, i, shape, "gy"), f32(gx, i, shape, "gx"),
+                                    f32(gweight, i, (norm.n_weights,), "gweight"), f32(gbias, i, (norm.n_bias,), "gbias"),
+                                    ws_ptr, ws_bytes, stream_of(i)), "tp_norm_bwd")
     return gx, gweight, gbias
 
 
@@ -224,26 +221,25 @@ class Dropout:
             self.handle = None
 
 
-def _dropout(name, drop, x, p, rng, site, y, stream):
-    N, dev = x.shape[0], x.device
-    _shape(x, (N, drop.dim), "input")
-    _shape(y, (N, drop.dim), "output")
-    _shape(rng, (2,), "rng")
-    _same_device(dev, rng=rng, output=y)
-    with _on(dev, stream):
-        y = torch.empty(N, drop.dim, dtype=torch.float32, device=dev) if y is None else y
-        check(getattr(load(), name)(drop.handle, N, _ptr(x, torch.float32, "input"), float(p),
-                                    _ptr(rng, torch.int64, "rng"), int(site), _ptr(y, torch.float32, "output"),
-                                    torch.cuda.current_stream(dev).cuda_stream), name)
+def _dropout(call, name, drop, x, p, rng, site, y, stream):
+    N = x.shape[0]
+    shape = (N, drop.dim)
+    if x.shape != shape:
+        raise ValueError(f"input must have shape {list(shape)}, got {list(x.shape)}")
+    i = device_index(x, "input")
+    with on(i, stream):
+        y = torch.empty(shape, dtype=torch.float32, device=x.device) if y is None else y
+        check(call(drop.handle, N, f32(x, i, shape, "input"), float(p), ptr(rng, torch.int64, i, (2,), "rng"), int(site),
+                   f32(y, i, shape, "output"), stream_of(i)), name)
     return y
 
 
 def tp_dropout_fwd(drop: Dropout, x, p: float, rng=None, site: int = 0, y=None, stream=None):
     """y = x with whole channels dropped with probability p and the rest scaled by 1/(1-p); rng is an int64
     CUDA tensor (seed, offset), site tells the calls of one step apart.  y may be x."""
-    return _dropout("tp_dropout_fwd", drop, x, p, rng, site, y, stream)
+    return _dropout(drop._lib.tp_dropout_fwd, "tp_dropout_fwd", drop, x, p, rng, site, y, stream)
 
 
 def tp_dropout_bwd(drop: Dropout, gy, p: float, rng=None, site: int = 0, gx=None, stream=None):
     """gx: the choice of tp_dropout_fwd with the same p, rng and site, drawn again, applied to gy."""
-    return _dropout("tp_dropout_bwd", drop, gy, p, rng, site, gx, stream)
+    return _dropout(drop._lib.tp_dropout_bwd, "tp_dropout_bwd", drop, gy, p, rng, site, gx, stream)

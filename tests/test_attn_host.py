@@ -183,10 +183,10 @@ def test_binding_refuses_what_it_cannot_pass_on(tp):
         tp.tp_norm_fwd(n, x, torch.zeros(4))
     with pytest.raises(ValueError, match="shape"):
         tp.tp_dropout_fwd(d, torch.zeros(2, 15), 0.0)
-    from equivariant_tensor_product_b200.attn import _rows
+    from equivariant_tensor_product_b200._marshal import rows
     meta = torch.zeros(4, 16)
     with pytest.raises(ValueError):
-        _rows(meta.t(), 16, 4, "q")
+        rows(meta.t(), 0, 16, 4, "q")
 
 
 def test_no_cpu_path_without_a_device(tp):
