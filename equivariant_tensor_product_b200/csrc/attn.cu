@@ -55,6 +55,7 @@ struct AttnArgs {
   int hw, groups;            // heads per warp (a power of two), head groups of a row
   int W;                     // warps that split a row's edges
   int row_ctas;              // CTAs of the rows; the windows' CTAs come after them
+  int rows;                  // rows of a CTA (of one head group); more than kAttnWarps / W are handed out in turn
   int hub, win, n_win;       // rows of more than hub edges go by windows (n_win = 0: no such rows)
   float* part;               // workspace [n_win][2][part_len]: partial rows of the windows
   int part_len;
@@ -88,7 +89,7 @@ struct AttnArgs {
   HeadMap mq, mv;
 };
 
-constexpr int kMinWindow = 128;
+constexpr int kMinWindow = 256;
 
 // The kernels of one call follow each other by programmatic dependent launch: a kernel lets the next
 // one be set up from its start on, and the next one waits here, before it touches anything that an
@@ -173,14 +174,28 @@ struct Task {
   bool write;                // false: a long row, which the windows deal with
 };
 
-// Number of tasks of this CTA.  Rows: one.  Windows: the heads of up to two rows, found here.
+// The tasks of this CTA.  Rows, one warp each: the CTA's warps take its rows as they get free, so that a
+// row of many edges holds up one warp and not its neighbours' next rows.  Rows of several warps or of a
+// whole CTA: one.  Windows: the heads of up to two long rows, found here.
+template <bool WIDE>
 struct Tasks {
-  int n, first, row0, row1;
+  int n, next, first, row0, row1;
+  int* ticket;
 
-  __device__ __forceinline__ Tasks(const AttnArgs& a, const int32_t* __restrict__ ptr, bool wide) {
-    __shared__ int found[2];
-    n = 1;
-    if ((int)blockIdx.x < a.row_ctas) return;
+  __device__ __forceinline__ Tasks(const AttnArgs& a, const int32_t* __restrict__ ptr) {
+    __shared__ int found[2], taken;
+    next = 0;
+    ticket = &taken;
+    if ((int)blockIdx.x < a.row_ctas) {
+      n = 1;
+      if (!WIDE && a.W == 1) {
+        n = a.rows;
+        if (threadIdx.x == 0) taken = kAttnWarps;
+        __syncthreads();
+        next = threadIdx.x >> 5;
+      }
+      return;
+    }
     first = ((int)blockIdx.x - a.row_ctas) * a.win;
     if (threadIdx.x < 64) {
       const int slot = threadIdx.x >> 5;
@@ -194,44 +209,54 @@ struct Tasks {
     __syncthreads();
     row0 = found[0];
     row1 = found[1];
-    n = 2 * (wide ? a.H : a.groups);
+    n = row0 < 0 && row1 < 0 ? 0 : 2 * (WIDE ? a.H : a.groups);
   }
 
-  __device__ __forceinline__ Task get(const AttnArgs& a, const int32_t* __restrict__ ptr, int i, bool wide) const {
-    Task t;
+  __device__ __forceinline__ bool get(const AttnArgs& a, const int32_t* __restrict__ ptr, Task& t) {
     const int warp = threadIdx.x >> 5;
+    if (next >= n) return false;
     t.part = nullptr;
     t.write = false;
-    t.row = a.N;
-    t.lo = t.hi = t.head0 = t.split = 0;
+    t.lo = t.hi = t.split = 0;
     t.W = 1;
     if ((int)blockIdx.x < a.row_ctas) {
-      if (wide) {
+      if (WIDE) {
         t.row = blockIdx.x / a.H;
         t.head0 = blockIdx.x - t.row * a.H;
+        next = n;
       } else {
-        const int unit = blockIdx.x * (kAttnWarps / a.W) + warp / a.W;
-        t.W = a.W;
-        t.split = warp % a.W;
-        t.row = unit / a.groups;
-        t.head0 = (unit - t.row * a.groups) * a.hw;
+        // one head group after the other: what a group reads of k and v stays in L2 for longer
+        const int blocks = a.row_ctas / a.groups, g = blockIdx.x / blocks, block = blockIdx.x - g * blocks;
+        t.head0 = g * a.hw;
+        if (a.W == 1) {
+          t.row = block * a.rows + next;
+          if ((threadIdx.x & 31) == 0) next = atomicAdd(ticket, 1);
+          next = __shfl_sync(kFull, next, 0);
+          if (t.row >= a.N) return false;
+        } else {
+          t.W = a.W;
+          t.split = warp % a.W;
+          t.row = block * a.rows + warp / a.W;
+          next = n;
+          if (t.row >= a.N) return true;
+        }
       }
-      if (t.row >= a.N) return t;
       t.lo = clamp_edge(__ldg(ptr + t.row), a.E);
       t.hi = clamp_edge(__ldg(ptr + t.row + 1), a.E);
       t.write = a.n_win == 0 || t.hi - t.lo <= a.hub;
       if (!t.write) t.hi = t.lo;
     } else {
-      const int per = wide ? a.H : a.groups, slot = i / per;
-      const int r = slot ? row1 : row0;
-      if (r < 0) return t;
-      t.row = r;
-      t.head0 = (i - slot * per) * (wide ? 1 : a.hw);
+      const int per = WIDE ? a.H : a.groups, slot = next / per;
+      if (next > 0) __syncthreads();     // the join buffer is free again
+      t.row = slot ? row1 : row0;
+      t.head0 = (next - slot * per) * (WIDE ? 1 : a.hw);
+      ++next;
+      if (t.row < 0) return true;
       t.write = true;
       t.part = a.part + ((int64_t)((int)blockIdx.x - a.row_ctas) * 2 + slot) * a.part_len;
       t.lo = max(__ldg(ptr + t.row), first);
       t.hi = min(min(__ldg(ptr + t.row + 1), first + a.win), a.E);
-      if (!wide) {
+      if (!WIDE) {
         t.W = kAttnWarps;
         t.split = warp;
       }
@@ -241,7 +266,7 @@ struct Tasks {
       t.lo += min(t.split * per, t.hi - t.lo);
       t.hi = min(t.hi, t.lo + per);
     }
-    return t;
+    return true;
   }
 };
 
@@ -250,24 +275,20 @@ struct Tasks {
 template <int V, bool WIDE>
 struct Lane {
   int h, G, gl, sub;
-  bool live;
+  bool live;                 // a head of its own, of a row that is this task's to write
 
-  __device__ __forceinline__ Lane(const AttnArgs& a, const Task& t) {
+  __device__ __forceinline__ Lane(const AttnArgs& a) : h(-1), live(false) {
     const int lane = threadIdx.x & 31;
-    if constexpr (WIDE) {
-      h = t.head0;
-      sub = 0;
-      G = blockDim.x;
-      gl = threadIdx.x;
-      live = t.write;
-    } else {
-      G = 32 / a.hw;
-      sub = lane / G;
-      gl = lane & (G - 1);
-      h = t.head0 + sub;
-      live = t.write && h < a.H;
-      h = min(h, a.H - 1);
-    }
+    G = WIDE ? blockDim.x : 32 / a.hw;
+    sub = WIDE ? 0 : lane / G;
+    gl = WIDE ? threadIdx.x : lane & (G - 1);
+  }
+  // Takes up a task; true if the head is another one than before.
+  __device__ __forceinline__ bool take(const AttnArgs& a, const Task& t) {
+    const int want = t.head0 + sub, was = h;
+    h = min(want, a.H - 1);
+    live = t.write && want < a.H;
+    return __any_sync(kFull, h != was);
   }
 
   __device__ __forceinline__ bool has(const HeadMap& m, int s) const { return (s * G + gl) * V < m.hd; }
@@ -363,6 +384,8 @@ __device__ __forceinline__ bool marked(float p) { return __float_as_uint(p) == 0
 
 template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_fwd(const __grid_constant__ AttnArgs a) {
+  // rows of k at a time: more where a lane holds but one chunk of them
+  constexpr int UA = SQ == 1 && !WIDE ? 8 : U;
   __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * SV + 2) * 32];
   let_next_launch();
   const int lane = threadIdx.x & 31;
@@ -370,28 +393,27 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   int turn = 0;
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  const Tasks tasks(a, a.rowptr, WIDE);
-  for (int task = 0; task < tasks.n; ++task) {
-    const Task t = tasks.get(a, a.rowptr, task, WIDE);
-    const Lane<V, WIDE> L(a, t);
+  Tasks<WIDE> tasks(a, a.rowptr);
+  Lane<V, WIDE> L(a);
+  const char *kp[SQ], *vp[SV];
+  for (Task t; tasks.get(a, a.rowptr, t);) {
     Vec<V> q[SQ], acc[SV];
-    const char *kp[SQ], *vp[SV];
     float m = -INFINITY, l = 0.0f;       // maximum of the group's logits; the lane's share of the sum
-    {
+    if (L.take(a, t)) {
       int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
 #pragma unroll
-      for (int s = 0; s < SQ; ++s) {
-        kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
-        q[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.q + oq[s]), t.row, a.ldq), L.live && L.has(a.mq, s));
-      }
+      for (int s = 0; s < SQ; ++s) kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
 #pragma unroll
-      for (int s = 0; s < SV; ++s) {
-        vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
-        acc[s] = zero_vec<V>();
-      }
+      for (int s = 0; s < SV; ++s) vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
     }
+    const int64_t k_to_q = reinterpret_cast<const char*>(a.q) - reinterpret_cast<const char*>(a.k);
+#pragma unroll
+    for (int s = 0; s < SQ; ++s)
+      q[s] = load_vec<V, true>(row_at(kp[s] + k_to_q, t.row, a.ldq), L.live && L.has(a.mq, s));
+#pragma unroll
+    for (int s = 0; s < SV; ++s) acc[s] = zero_vec<V>();
     for (int base = t.lo; base < t.hi; base += 32) {
       const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, a.hw);
       const uint32_t live = __ballot_sync(kFull, mine.j >= 0);
@@ -405,12 +427,12 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         B.c[at] = mine.keep;
       }
       __syncwarp();
-      // (a) logits.  The last round repeats the last edge where there are fewer than U left.
-      for (int t0 = 0; t0 < n; t0 += U) {
-        float dot[U];
-        Vec<V> x[U][SQ];
+      // (a) logits.  The last round repeats the last edge where there are fewer left.
+      for (int t0 = 0; t0 < n; t0 += UA) {
+        float dot[UA];
+        Vec<V> x[UA][SQ];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < UA; ++u) {
           const int j = B.row[min(t0 + u, n - 1)];
 #pragma unroll
           for (int s = 0; s < SQ; ++s)
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
                                            : load_vec<V, true>(row_at(kp[s], j, a.ldk), L.has(a.mq, s));
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < UA; ++u) {
           dot[u] = 0.0f;
 #pragma unroll
           for (int s = 0; s < SQ; ++s)
@@ -428,7 +450,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         L.sum(dot, join, turn);
         if (L.first() == 0) {
 #pragma unroll
-          for (int u = 0; u < U; ++u) B.f[min(t0 + u, n - 1) * a.hw + L.sub] = dot[u];
+          for (int u = 0; u < UA; ++u) B.f[min(t0 + u, n - 1) * a.hw + L.sub] = dot[u];
         }
       }
       __syncwarp();
@@ -540,7 +562,6 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         if (a.lse && L.gl == 0) a.lse[(int64_t)t.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
       }
     }
-    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
@@ -556,34 +577,38 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   int turn = 0;
   DropKey key{};
   if (a.drop.rng) key = drop_key(a.drop);
-  const Tasks tasks(a, a.rowptr, WIDE);
-  for (int task = 0; task < tasks.n; ++task) {
-    const Task t = tasks.get(a, a.rowptr, task, WIDE);
-    const Lane<V, WIDE> L(a, t);
+  Tasks<WIDE> tasks(a, a.rowptr);
+  Lane<V, WIDE> L(a);
+  const char *kp[SQ], *vp[SV];
+  for (Task t; tasks.get(a, a.rowptr, t);) {
     Vec<V> q[SQ], gy[SV], acc[SQ];
-    const char *kp[SQ], *vp[SV];
     float delta[2 * U];
 #pragma unroll
     for (int u = 0; u < 2 * U; ++u) delta[u] = 0.0f;
-    {
+    if (L.take(a, t)) {
       int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
 #pragma unroll
-      for (int s = 0; s < SQ; ++s) {
-        kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
-        q[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.q + oq[s]), t.row, a.ldq), L.live && L.has(a.mq, s));
-        acc[s] = zero_vec<V>();
-      }
+      for (int s = 0; s < SQ; ++s) kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
 #pragma unroll
-      for (int s = 0; s < SV; ++s) {
-        const bool on = L.live && L.has(a.mv, s);
-        vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
-        gy[s] = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.gy + ov[s]), t.row, a.dv * 4u), on);
-        const Vec<V> y = load_vec<V, true>(row_at(reinterpret_cast<const char*>(a.y_in + ov[s]), t.row, a.dv * 4u), on);
+      for (int s = 0; s < SV; ++s) vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
+    }
+    const int64_t k_to_q = reinterpret_cast<const char*>(a.q) - reinterpret_cast<const char*>(a.k);
+    const int64_t v_to_gy = reinterpret_cast<const char*>(a.gy) - reinterpret_cast<const char*>(a.v);
+    const int64_t v_to_y = reinterpret_cast<const char*>(a.y_in) - reinterpret_cast<const char*>(a.v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
-      }
+    for (int s = 0; s < SQ; ++s) {
+      q[s] = load_vec<V, true>(row_at(kp[s] + k_to_q, t.row, a.ldq), L.live && L.has(a.mq, s));
+      acc[s] = zero_vec<V>();
+    }
+#pragma unroll
+    for (int s = 0; s < SV; ++s) {
+      const bool on = L.live && L.has(a.mv, s);
+      gy[s] = load_vec<V, true>(row_at(vp[s] + v_to_gy, t.row, a.dv * 4u), on);
+      const Vec<V> y = load_vec<V, true>(row_at(vp[s] + v_to_y, t.row, a.dv * 4u), on);
+#pragma unroll
+      for (int i = 0; i < V; ++i) delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
     }
     L.sum(delta, join, turn);
     const float del = delta[0];
@@ -695,7 +720,6 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + oq, acc[s]);
       }
     }
-    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
@@ -771,28 +795,25 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   const Batch B = batch_of_warp(a.hw);
   float2* const w2 = reinterpret_cast<float2*>(B.f);
   const int e_lo = max(__ldg(a.rowptr), 0), e_hi = min(__ldg(a.rowptr + a.N), a.E);
-  const Tasks tasks(a, a.colptr, WIDE);
+  Tasks<WIDE> tasks(a, a.colptr);
   wait_for_previous();
-  for (int task = 0; task < tasks.n; ++task) {
-    const Task t = tasks.get(a, a.colptr, task, WIDE);
-    const Lane<V, WIDE> L(a, t);
+  Lane<V, WIDE> L(a);
+  const char *qp[SQ], *gp[SV];
+  for (Task t; tasks.get(a, a.colptr, t);) {
     Vec<V> ak[SQ], av[SV];
-    const char *qp[SQ], *gp[SV];
-    {
+    if (L.take(a, t)) {
       int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
 #pragma unroll
-      for (int s = 0; s < SQ; ++s) {
-        qp[s] = reinterpret_cast<const char*>(a.q + oq[s]);
-        ak[s] = zero_vec<V>();
-      }
+      for (int s = 0; s < SQ; ++s) qp[s] = reinterpret_cast<const char*>(a.q + oq[s]);
 #pragma unroll
-      for (int s = 0; s < SV; ++s) {
-        gp[s] = reinterpret_cast<const char*>(a.gy + ov[s]);
-        av[s] = zero_vec<V>();
-      }
+      for (int s = 0; s < SV; ++s) gp[s] = reinterpret_cast<const char*>(a.gy + ov[s]);
     }
+#pragma unroll
+    for (int s = 0; s < SQ; ++s) ak[s] = zero_vec<V>();
+#pragma unroll
+    for (int s = 0; s < SV; ++s) av[s] = zero_vec<V>();
     for (int base = t.lo; base < t.hi; base += 32) {
       int e = -1, i = -1;
       if (base + lane < t.hi) {
@@ -895,7 +916,6 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         else if (a.gv) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + ov, av[s]);
       }
     }
-    if (task + 1 < tasks.n) __syncthreads();   // the join buffer is free again
   }
 }
 
@@ -1085,12 +1105,21 @@ size_t hist_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H 
 
 template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
 cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s) {
+  // more than 48 KB with the kernel's own arrays (the largest: 17 KB) has to be asked for
+  auto allow = [](auto kernel, size_t smem) {
+    return smem <= 30 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  };
   size_t smem = batch_bytes(threads, a.hw);
   const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
   if (pass == kSend) {
     if (a.hist_ctas > 0) smem = std::max(smem, hist_bytes(a));
+    cudaError_t e = allow(k_attn_bwd_send<V, SQ, SV, U, LOOSE, WIDE>, smem);
+    if (e != cudaSuccess) return e;
     return launch_after(k_attn_bwd_send<V, SQ, SV, U, LOOSE, WIDE>, grid + (unsigned)a.hist_ctas, threads, smem, s, a);
   }
+  cudaError_t e = pass == kFwd ? allow(k_attn_fwd<V, SQ, SV, U, LOOSE, WIDE>, smem)
+                               : allow(k_attn_bwd_recv<V, SQ, SV, U, LOOSE, WIDE>, smem);
+  if (e != cudaSuccess) return e;
   if (pass == kFwd) k_attn_fwd<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
   else k_attn_bwd_recv<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
   count_launches(1);
@@ -1130,8 +1159,10 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)a.N * a.groups;
   a.W = 1;
   while (a.W < kAttnWarps && units * a.W < 148 * 8 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
-  const int per = kAttnWarps / a.W;
-  a.row_ctas = (int)((units + per - 1) / per);
+  a.rows = kAttnWarps / a.W;
+  // with one warp a row, up to 16 rows a CTA to choose from, as long as every SM has its CTAs
+  while (a.W == 1 && a.rows < 16 && units > (int64_t)148 * 16 * a.rows) a.rows *= 2;
+  a.row_ctas = (int)((a.N + a.rows - 1) / a.rows) * a.groups;
   switch (need) {
     case 1: return launch_form<V, 1, 4>(pass, a, cq, cv, s);
     case 2: return launch_form<V, 2, 4>(pass, a, cq, cv, s);

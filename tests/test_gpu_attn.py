@@ -85,7 +85,8 @@ SHAPES = [
     ("64x0e+64x1o+64x2e+64x3o", "64x0e", 32), ("32x0o", "32x1e+32x0o", 32), ("12x0e+24x0e", "12x1o+12x1e", 12),
     ("16x0e+16x2e", "160x0e+32x1o", 1), ("33x0e+33x1o+33x2e", "33x0e+33x1o", 1), ("128x0e+128x1o", "128x0e+128x1o+128x2e", 1),
     ("100x0e+100x3o", "118x0e+118x2e", 1), ("600x0e", "300x1o+64x0e", 2), ("4x0e", "512x3o", 1), ("301x0e", "301x3o", 1),
-    ("128x0e+128x0o+128x1o+128x1e+128x2e+128x3o", "8x0e", 1),
+    ("128x0e+128x0o+128x1o+128x1e+128x2e+128x3o", "8x0e", 1), ("32x0e+32x1o+32x2e+32x3o", "32x0e+32x1o+32x2e+32x3o", 8),
+    ("128x0e+128x1o", "512x0e", 32), ("256x0e", "256x1o+128x0e", 16),
 ]
 
 
