@@ -55,7 +55,6 @@ struct AttnArgs {
   int hw, groups;            // heads per warp (a power of two), head groups of a row
   int W;                     // warps that split a row's edges
   int row_ctas;              // CTAs of the rows; the windows' CTAs come after them
-  int rows;                  // rows of a CTA (of one head group); more than kAttnWarps / W are handed out in turn
   int hub, win, n_win;       // rows of more than hub edges go by windows (n_win = 0: no such rows)
   float* part;               // workspace [n_win][2][part_len]: partial rows of the windows
   int part_len;
@@ -88,6 +87,35 @@ struct AttnArgs {
   int hist_ctas, hist_copies, hist_lanes;   // hist_ctas = 0 in the sender pass: no table CTAs behind it
   HeadMap mq, mv;
 };
+
+enum Pass { kFwd, kRecv, kSend };
+
+// Rows in flight (U) and CTAs a SM, which holds the registers down, for S chunks a lane.  Both hide the
+// latency of the gathers and both want registers; what is first in short supply differs by pass.  Measured
+// with 16-byte chunks, 46,080 edges of 288 floats and 3.0M edges of 1,152 floats (S = 3), 162,892 edges of
+// 1,024 floats (S = 4):
+//   forward  S = 3: U 4 at 4 CTAs 15.8 us / 3.78 ms, U 4 at 5 18.2 / 4.08, U 2 at 5 20.0 / 4.54
+//            S = 4: U 2 at 5 CTAs 103 us, U 1 at 6 161
+//   receiver S = 3: U 2 at 4 CTAs 17.7 us / 4.07 ms, U 4 at 3 18.0 / 4.85, U 2 at 5 21.3 / 4.80
+//            S = 4: U 2 at 4 CTAs 116 us, U 2 at 3 121, U 1 at 5 126
+//   sender   S = 3: U 4 at 3 CTAs 16.1 us / 4.28 ms, U 2 at 4 18.4 / 4.21, U 2 at 5 20.1 / 4.01
+//            S = 4: U 1 at 5 CTAs 97 us, U 2 at 4 103
+// and with 4-byte chunks, 100,003 edges of 189 floats (S = 4): forward U 4 at 5 CTAs 45 us, at 6 49; receiver
+// U 2 at 5 47, U 4 at 5 53; sender U 2 at 6 33, at 5 37.
+__host__ __device__ constexpr int rows_at_once(Pass pass, int V, int S, bool wide) {
+  if (wide) return S <= 4 ? 2 : 1;
+  if (V == 1) return S <= 3 || (S == 4 && pass == kFwd) ? 4 : S == 4 || pass != kRecv ? 2 : 1;
+  if (S <= 2) return 4;
+  if (S == 3) return pass == kRecv ? 2 : 4;
+  return S == 4 && pass != kSend ? 2 : 1;
+}
+__host__ __device__ constexpr int ctas_per_sm(Pass pass, int V, int S) {
+  if (S >= 6) return S == 6 ? 3 : 2;
+  if (V == 1) return pass == kSend ? 6 : 5;
+  if (S <= 2) return 4;
+  if (S == 3) return pass == kSend ? 3 : 4;
+  return pass == kRecv ? 4 : 5;
+}
 
 constexpr int kMinWindow = 256;
 
@@ -134,9 +162,9 @@ __device__ __forceinline__ Vec<V> load_vec(const char* p, bool on) {
   return r;
 }
 
-// Byte address of row j for a lane's chunk: one 32 x 32 -> 64 bit multiply-add.
-__device__ __forceinline__ const char* row_at(const char* p, int j, uint32_t row_bytes) {
-  return p + (uint64_t)(uint32_t)j * row_bytes;
+// Byte address of row j: one 32 x 32 -> 64 bit multiply-add.  A lane's chunks lie at 32-bit offsets from it.
+__device__ __forceinline__ const char* row_at(const float* p, int j, uint32_t row_bytes) {
+  return reinterpret_cast<const char*>(p) + (uint64_t)(uint32_t)j * row_bytes;
 }
 
 template <int V>
@@ -174,28 +202,16 @@ struct Task {
   bool write;                // false: a long row, which the windows deal with
 };
 
-// The tasks of this CTA.  Rows, one warp each: the CTA's warps take its rows as they get free, so that a
-// row of many edges holds up one warp and not its neighbours' next rows.  Rows of several warps or of a
-// whole CTA: one.  Windows: the heads of up to two long rows, found here.
+// The tasks of this CTA.  Rows: one.  Windows: the heads of up to two long rows, found here.
 template <bool WIDE>
 struct Tasks {
   int n, next, first, row0, row1;
-  int* ticket;
 
   __device__ __forceinline__ Tasks(const AttnArgs& a, const int32_t* __restrict__ ptr) {
-    __shared__ int found[2], taken;
+    __shared__ int found[2];
     next = 0;
-    ticket = &taken;
-    if ((int)blockIdx.x < a.row_ctas) {
-      n = 1;
-      if (!WIDE && a.W == 1) {
-        n = a.rows;
-        if (threadIdx.x == 0) taken = kAttnWarps;
-        __syncthreads();
-        next = threadIdx.x >> 5;
-      }
-      return;
-    }
+    n = 1;
+    if ((int)blockIdx.x < a.row_ctas) return;
     first = ((int)blockIdx.x - a.row_ctas) * a.win;
     if (threadIdx.x < 64) {
       const int slot = threadIdx.x >> 5;
@@ -220,26 +236,18 @@ struct Tasks {
     t.lo = t.hi = t.split = 0;
     t.W = 1;
     if ((int)blockIdx.x < a.row_ctas) {
+      next = 1;
       if (WIDE) {
         t.row = blockIdx.x / a.H;
         t.head0 = blockIdx.x - t.row * a.H;
-        next = n;
       } else {
         // one head group after the other: what a group reads of k and v stays in L2 for longer
-        const int blocks = a.row_ctas / a.groups, g = blockIdx.x / blocks, block = blockIdx.x - g * blocks;
+        const int blocks = a.row_ctas / a.groups, g = blockIdx.x / blocks;
         t.head0 = g * a.hw;
-        if (a.W == 1) {
-          t.row = block * a.rows + next;
-          if ((threadIdx.x & 31) == 0) next = atomicAdd(ticket, 1);
-          next = __shfl_sync(kFull, next, 0);
-          if (t.row >= a.N) return false;
-        } else {
-          t.W = a.W;
-          t.split = warp % a.W;
-          t.row = block * a.rows + warp / a.W;
-          next = n;
-          if (t.row >= a.N) return true;
-        }
+        t.W = a.W;
+        t.split = warp % a.W;
+        t.row = ((int)blockIdx.x - g * blocks) * (kAttnWarps / a.W) + warp / a.W;
+        if (t.row >= a.N) return true;
       }
       t.lo = clamp_edge(__ldg(ptr + t.row), a.E);
       t.hi = clamp_edge(__ldg(ptr + t.row + 1), a.E);
@@ -292,11 +300,11 @@ struct Lane {
   }
 
   __device__ __forceinline__ bool has(const HeadMap& m, int s) const { return (s * G + gl) * V < m.hd; }
-  // Offsets of the chunks in a row; a chunk the lane lacks is given the row's first float.
+  // Byte offsets of the chunks in a row; a chunk the lane lacks is given the row's first.
   template <int S>
-  __device__ __forceinline__ void offsets(const HeadMap& m, int (&o)[S]) const {
+  __device__ __forceinline__ void offsets(const HeadMap& m, uint32_t (&o)[S]) const {
 #pragma unroll
-    for (int s = 0; s < S; ++s) o[s] = max(slot_offset(m, h, (s * G + gl) * V), 0);
+    for (int s = 0; s < S; ++s) o[s] = 4u * max(slot_offset(m, h, (s * G + gl) * V), 0);
   }
 
   // The lane's part in a batch of 32 edges x the warp's heads: entries lane' + 32 i of [edge][head].
@@ -382,10 +390,11 @@ size_t batch_bytes(int threads, int hw) { return (size_t)(threads / 32) * (96 + 
 // a sum, whatever it holds.  Such an entry is marked with -0, which no probability is.
 __device__ __forceinline__ bool marked(float p) { return __float_as_uint(p) == 0x80000000u; }
 
-template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_fwd(const __grid_constant__ AttnArgs a) {
+template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kFwd, V, SV)) k_attn_fwd(const __grid_constant__ AttnArgs a) {
+  constexpr int U = rows_at_once(kFwd, V, SV, WIDE);
   // rows of k at a time: more where a lane holds but one chunk of them
-  constexpr int UA = SQ == 1 && !WIDE ? 8 : U;
+  constexpr int UA = WIDE ? U : SQ == 1 || (SQ == 2 && V == 1) ? 8 : SQ == 2 ? 4 : U;
   __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * SV + 2) * 32];
   let_next_launch();
   const int lane = threadIdx.x & 31;
@@ -395,23 +404,18 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   if (a.drop.rng) key = drop_key(a.drop);
   Tasks<WIDE> tasks(a, a.rowptr);
   Lane<V, WIDE> L(a);
-  const char *kp[SQ], *vp[SV];
+  uint32_t oq[SQ], ov[SV];
   for (Task t; tasks.get(a, a.rowptr, t);) {
     Vec<V> q[SQ], acc[SV];
     float m = -INFINITY, l = 0.0f;       // maximum of the group's logits; the lane's share of the sum
     if (L.take(a, t)) {
-      int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
-#pragma unroll
-      for (int s = 0; s < SQ; ++s) kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
-#pragma unroll
-      for (int s = 0; s < SV; ++s) vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
     }
-    const int64_t k_to_q = reinterpret_cast<const char*>(a.q) - reinterpret_cast<const char*>(a.k);
+    const char* q_row = row_at(a.q, t.row, a.ldq);
 #pragma unroll
     for (int s = 0; s < SQ; ++s)
-      q[s] = load_vec<V, true>(row_at(kp[s] + k_to_q, t.row, a.ldq), L.live && L.has(a.mq, s));
+      q[s] = load_vec<V, true>(q_row + oq[s], L.live && L.has(a.mq, s));
 #pragma unroll
     for (int s = 0; s < SV; ++s) acc[s] = zero_vec<V>();
     for (int base = t.lo; base < t.hi; base += 32) {
@@ -433,11 +437,11 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         Vec<V> x[UA][SQ];
 #pragma unroll
         for (int u = 0; u < UA; ++u) {
-          const int j = B.row[min(t0 + u, n - 1)];
+          const char* row = row_at(a.k, B.row[min(t0 + u, n - 1)], a.ldk);
 #pragma unroll
           for (int s = 0; s < SQ; ++s)
-            x[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(kp[s], j, a.ldk), true)
-                                           : load_vec<V, true>(row_at(kp[s], j, a.ldk), L.has(a.mq, s));
+            x[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row + oq[s], true)
+                                           : load_vec<V, true>(row + oq[s], L.has(a.mq, s));
         }
 #pragma unroll
         for (int u = 0; u < UA; ++u) {
@@ -490,11 +494,11 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
         Vec<V> x[U][SV];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int j = B.row[min(t0 + u, n - 1)];
+          const char* row = row_at(a.v, B.row[min(t0 + u, n - 1)], a.ldv);
 #pragma unroll
           for (int s = 0; s < SV; ++s)
-            x[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(vp[s], j, a.ldv), true)
-                                           : load_vec<V, true>(row_at(vp[s], j, a.ldv), L.has(a.mv, s));
+            x[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row + ov[s], true)
+                                           : load_vec<V, true>(row + ov[s], L.has(a.mv, s));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -538,13 +542,10 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
       }
     }
     if (L.live && t.split == 0) {
-      int64_t ov[SV];
-#pragma unroll
-      for (int s = 0; s < SV; ++s) ov[s] = reinterpret_cast<const float*>(vp[s]) - a.v;
       if (t.part) {
 #pragma unroll
         for (int s = 0; s < SV; ++s)
-          if (L.has(a.mv, s)) store_vec<V>(t.part + ov[s], acc[s]);
+          if (L.has(a.mv, s)) store_vec<V>(t.part + ov[s] / 4, acc[s]);
         if (L.gl == 0) {
           t.part[a.part_len - 2 * a.H + L.h] = m;
           t.part[a.part_len - a.H + L.h] = l;
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
           if (!L.has(a.mv, s)) continue;
 #pragma unroll
           for (int i = 0; i < V; ++i) acc[s].x[i] *= f;
-          store_vec<V>(a.y + (int64_t)t.row * a.dv + ov[s], acc[s]);
+          store_vec<V>(a.y + (int64_t)t.row * a.dv + ov[s] / 4, acc[s]);
         }
         if (a.lse && L.gl == 0) a.lse[(int64_t)t.row * a.H + L.h] = none ? -INFINITY : m + logf(l);
       }
@@ -567,8 +568,9 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 
 // Backward, receiver order: gq, and for the sender pass and gtable (ds, r p) of every live edge and head
 // and the receiver of every edge.
-template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_recv(const __grid_constant__ AttnArgs a) {
+template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kRecv, V, SV)) k_attn_bwd_recv(const __grid_constant__ AttnArgs a) {
+  constexpr int U = rows_at_once(kRecv, V, SV, WIDE);
   __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * 2 * U : kAttnWarps * V * SQ * 32];
   let_next_launch();
   const int lane = threadIdx.x & 31;
@@ -579,34 +581,27 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   if (a.drop.rng) key = drop_key(a.drop);
   Tasks<WIDE> tasks(a, a.rowptr);
   Lane<V, WIDE> L(a);
-  const char *kp[SQ], *vp[SV];
+  uint32_t oq[SQ], ov[SV];
   for (Task t; tasks.get(a, a.rowptr, t);) {
     Vec<V> q[SQ], gy[SV], acc[SQ];
     float delta[2 * U];
 #pragma unroll
     for (int u = 0; u < 2 * U; ++u) delta[u] = 0.0f;
     if (L.take(a, t)) {
-      int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
-#pragma unroll
-      for (int s = 0; s < SQ; ++s) kp[s] = reinterpret_cast<const char*>(a.k + oq[s]);
-#pragma unroll
-      for (int s = 0; s < SV; ++s) vp[s] = reinterpret_cast<const char*>(a.v + ov[s]);
     }
-    const int64_t k_to_q = reinterpret_cast<const char*>(a.q) - reinterpret_cast<const char*>(a.k);
-    const int64_t v_to_gy = reinterpret_cast<const char*>(a.gy) - reinterpret_cast<const char*>(a.v);
-    const int64_t v_to_y = reinterpret_cast<const char*>(a.y_in) - reinterpret_cast<const char*>(a.v);
+    const char *q_row = row_at(a.q, t.row, a.ldq), *gy_row = row_at(a.gy, t.row, a.dv * 4u), *y_row = row_at(a.y_in, t.row, a.dv * 4u);
 #pragma unroll
     for (int s = 0; s < SQ; ++s) {
-      q[s] = load_vec<V, true>(row_at(kp[s] + k_to_q, t.row, a.ldq), L.live && L.has(a.mq, s));
+      q[s] = load_vec<V, true>(q_row + oq[s], L.live && L.has(a.mq, s));
       acc[s] = zero_vec<V>();
     }
 #pragma unroll
     for (int s = 0; s < SV; ++s) {
       const bool on = L.live && L.has(a.mv, s);
-      gy[s] = load_vec<V, true>(row_at(vp[s] + v_to_gy, t.row, a.dv * 4u), on);
-      const Vec<V> y = load_vec<V, true>(row_at(vp[s] + v_to_y, t.row, a.dv * 4u), on);
+      gy[s] = load_vec<V, true>(gy_row + ov[s], on);
+      const Vec<V> y = load_vec<V, true>(y_row + ov[s], on);
 #pragma unroll
       for (int i = 0; i < V; ++i) delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
     }
@@ -644,14 +639,15 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int j = B.row[min(t0 + u, n - 1)];
+          const char *k_row = row_at(a.k, j, a.ldk), *v_row = row_at(a.v, j, a.ldv);
 #pragma unroll
           for (int s = 0; s < SQ; ++s)
-            kk[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(kp[s], j, a.ldk), true)
-                                            : load_vec<V, true>(row_at(kp[s], j, a.ldk), L.has(a.mq, s));
+            kk[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(k_row + oq[s], true)
+                                            : load_vec<V, true>(k_row + oq[s], L.has(a.mq, s));
 #pragma unroll
           for (int s = 0; s < SV; ++s)
-            vv[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(vp[s], j, a.ldv), true)
-                                            : load_vec<V, true>(row_at(vp[s], j, a.ldv), L.has(a.mv, s));
+            vv[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(v_row + ov[s], true)
+                                            : load_vec<V, true>(v_row + ov[s], L.has(a.mv, s));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -710,14 +706,13 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 #pragma unroll
       for (int s = 0; s < SQ; ++s) {
         if (!L.has(a.mq, s)) continue;
-        const int64_t oq = reinterpret_cast<const float*>(kp[s]) - a.k;
         if (t.part) {
-          store_vec<V>(t.part + oq, acc[s]);
+          store_vec<V>(t.part + oq[s] / 4, acc[s]);
           continue;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[s].x[i] *= a.scale;
-        store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + oq, acc[s]);
+        store_vec<V>(a.gq + (int64_t)t.row * a.ldgq + oq[s] / 4, acc[s]);
       }
     }
   }
@@ -782,8 +777,9 @@ __device__ __forceinline__ void table_sum(const AttnArgs& a, int o) {
 }
 
 // Backward, sender order: gk[j] = scale sum ds q[i], gv[j] = sum r p gy[i] over the edges that leave j.
-template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn_bwd_send(const __grid_constant__ AttnArgs a) {
+template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kSend, V, SV)) k_attn_bwd_send(const __grid_constant__ AttnArgs a) {
+  constexpr int U = rows_at_once(kSend, V, SV, WIDE);
   __shared__ float join[WIDE ? 1 : kAttnWarps * V * (SQ + SV) * 32];
   let_next_launch();
   if ((int)blockIdx.x >= a.row_ctas + a.n_win) {
@@ -798,17 +794,12 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
   Tasks<WIDE> tasks(a, a.colptr);
   wait_for_previous();
   Lane<V, WIDE> L(a);
-  const char *qp[SQ], *gp[SV];
+  uint32_t oq[SQ], ov[SV];
   for (Task t; tasks.get(a, a.colptr, t);) {
     Vec<V> ak[SQ], av[SV];
     if (L.take(a, t)) {
-      int oq[SQ], ov[SV];
       L.offsets(a.mq, oq);
       L.offsets(a.mv, ov);
-#pragma unroll
-      for (int s = 0; s < SQ; ++s) qp[s] = reinterpret_cast<const char*>(a.q + oq[s]);
-#pragma unroll
-      for (int s = 0; s < SV; ++s) gp[s] = reinterpret_cast<const char*>(a.gy + ov[s]);
     }
 #pragma unroll
     for (int s = 0; s < SQ; ++s) ak[s] = zero_vec<V>();
@@ -843,14 +834,15 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int r = B.row[min(t0 + u, n - 1)];
+          const char *q_row = row_at(a.q, r, a.ldq), *gy_row = row_at(a.gy, r, a.dv * 4u);
 #pragma unroll
           for (int s = 0; s < SQ; ++s)
-            qq[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(row_at(qp[s], r, a.ldq), true)
-                                            : load_vec<V, true>(row_at(qp[s], r, a.ldq), L.has(a.mq, s));
+            qq[u][s] = s < SQ - 1 && !LOOSE ? load_vec<V, false>(q_row + oq[s], true)
+                                            : load_vec<V, true>(q_row + oq[s], L.has(a.mq, s));
 #pragma unroll
           for (int s = 0; s < SV; ++s)
-            gg[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(row_at(gp[s], r, a.dv * 4u), true)
-                                            : load_vec<V, true>(row_at(gp[s], r, a.dv * 4u), L.has(a.mv, s));
+            gg[u][s] = s < SV - 1 && !LOOSE ? load_vec<V, false>(gy_row + ov[s], true)
+                                            : load_vec<V, true>(gy_row + ov[s], L.has(a.mv, s));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -899,21 +891,19 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads) k_attn
 #pragma unroll
       for (int s = 0; s < SQ; ++s) {
         if (!L.has(a.mq, s)) continue;
-        const int64_t oq = reinterpret_cast<const float*>(qp[s]) - a.q;
         if (t.part) {
-          store_vec<V>(t.part + oq, ak[s]);
+          store_vec<V>(t.part + oq[s] / 4, ak[s]);
         } else if (a.gk) {
 #pragma unroll
           for (int i = 0; i < V; ++i) ak[s].x[i] *= a.scale;
-          store_vec<V>(a.gk + (int64_t)t.row * a.ldgk + oq, ak[s]);
+          store_vec<V>(a.gk + (int64_t)t.row * a.ldgk + oq[s] / 4, ak[s]);
         }
       }
 #pragma unroll
       for (int s = 0; s < SV; ++s) {
         if (!L.has(a.mv, s)) continue;
-        const int64_t ov = reinterpret_cast<const float*>(gp[s]) - a.gy;
-        if (t.part) store_vec<V>(t.part + a.dq + ov, av[s]);
-        else if (a.gv) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + ov, av[s]);
+        if (t.part) store_vec<V>(t.part + a.dq + ov[s] / 4, av[s]);
+        else if (a.gv) store_vec<V>(a.gv + (int64_t)t.row * a.ldgv + ov[s] / 4, av[s]);
       }
     }
   }
@@ -1081,8 +1071,6 @@ tp_status_t cuda_status(cudaError_t e, const char* where) {
   return e == cudaSuccess ? TP_OK : set_failure(TP_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
 }
 
-enum Pass { kFwd, kRecv, kSend };
-
 // Launches `kernel` after the call's previous kernel (see let_next_launch).
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
@@ -1103,7 +1091,7 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_
 // Shared memory of a table_part CTA.
 size_t hist_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H * a.hist_copies; }
 
-template <int V, int SQ, int SV, int U, bool LOOSE, bool WIDE>
+template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
 cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s) {
   // more than 48 KB with the kernel's own arrays (the largest: 17 KB) has to be asked for
   auto allow = [](auto kernel, size_t smem) {
@@ -1113,28 +1101,35 @@ cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s
   const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
   if (pass == kSend) {
     if (a.hist_ctas > 0) smem = std::max(smem, hist_bytes(a));
-    cudaError_t e = allow(k_attn_bwd_send<V, SQ, SV, U, LOOSE, WIDE>, smem);
+    cudaError_t e = allow(k_attn_bwd_send<V, SQ, SV, LOOSE, WIDE>, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(k_attn_bwd_send<V, SQ, SV, U, LOOSE, WIDE>, grid + (unsigned)a.hist_ctas, threads, smem, s, a);
+    return launch_after(k_attn_bwd_send<V, SQ, SV, LOOSE, WIDE>, grid + (unsigned)a.hist_ctas, threads, smem, s, a);
   }
-  cudaError_t e = pass == kFwd ? allow(k_attn_fwd<V, SQ, SV, U, LOOSE, WIDE>, smem)
-                               : allow(k_attn_bwd_recv<V, SQ, SV, U, LOOSE, WIDE>, smem);
+  cudaError_t e = pass == kFwd ? allow(k_attn_fwd<V, SQ, SV, LOOSE, WIDE>, smem)
+                               : allow(k_attn_bwd_recv<V, SQ, SV, LOOSE, WIDE>, smem);
   if (e != cudaSuccess) return e;
-  if (pass == kFwd) k_attn_fwd<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
-  else k_attn_bwd_recv<V, SQ, SV, U, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
+  if (pass == kFwd) k_attn_fwd<V, SQ, SV, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
+  else k_attn_bwd_recv<V, SQ, SV, LOOSE, WIDE><<<grid, threads, smem, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
 
-// Three forms of the kernels for S chunks a lane: rows of q with a single chunk a lane (logits from a few
-// scalars), rows of q and v that both fill S - 1 chunks of every lane, and any others, where every read
-// asks whether the lane has the chunk.
-template <int V, int S, int U>
+// The forms of the kernels for S chunks of v a lane: q with one or two chunks (logits from a few channels) or
+// with S, where every lane has all but the last of each; and any others, where every read asks whether the
+// lane has the chunk (100,003 edges with 28 floats a head of q and 63 of v, which fill two and four
+// chunks: receiver pass 54 us in that form).
+template <int V, int S>
 cudaError_t launch_form(Pass pass, const AttnArgs& a, int cq, int cv, cudaStream_t s) {
-  const int G = 32 / a.hw, full = (S - 1) * G;
-  if (cv >= full && cq <= G) return launch_one<V, 1, S, U, false, false>(pass, a, kAttnThreads, s);
-  if (cv >= full && cq >= full) return launch_one<V, S, S, U, false, false>(pass, a, kAttnThreads, s);
-  return launch_one<V, S, S, U, true, false>(pass, a, kAttnThreads, s);
+  const int G = 32 / a.hw;
+  auto fills = [G](int chunks, int slots) { return chunks >= (slots - 1) * G && chunks <= slots * G; };
+  if (fills(cv, S)) {
+    if (fills(cq, 1)) return launch_one<V, 1, S, false, false>(pass, a, kAttnThreads, s);
+    if constexpr (S > 2) {
+      if (fills(cq, 2)) return launch_one<V, 2, S, false, false>(pass, a, kAttnThreads, s);
+    }
+    if (fills(cq, S)) return launch_one<V, S, S, false, false>(pass, a, kAttnThreads, s);
+  }
+  return launch_one<V, S, S, true, false>(pass, a, kAttnThreads, s);
 }
 
 template <int V>
@@ -1147,8 +1142,8 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
     a.groups = a.H;
     a.W = 1;
     a.row_ctas = a.N * a.H;
-    if (chunks <= 4 * threads) return launch_one<V, 4, 4, 2, true, true>(pass, a, threads, s);
-    return launch_one<V, 8, 8, 1, true, true>(pass, a, threads, s);
+    if (chunks <= 4 * threads) return launch_one<V, 4, 4, true, true>(pass, a, threads, s);
+    return launch_one<V, 8, 8, true, true>(pass, a, threads, s);
   }
   // as many heads in a warp as leave a lane at most four chunks
   int hw = 1;
@@ -1159,18 +1154,16 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)a.N * a.groups;
   a.W = 1;
   while (a.W < kAttnWarps && units * a.W < 148 * 8 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
-  a.rows = kAttnWarps / a.W;
-  // with one warp a row, up to 16 rows a CTA to choose from, as long as every SM has its CTAs
-  while (a.W == 1 && a.rows < 16 && units > (int64_t)148 * 16 * a.rows) a.rows *= 2;
-  a.row_ctas = (int)((a.N + a.rows - 1) / a.rows) * a.groups;
+  const int per = kAttnWarps / a.W;
+  a.row_ctas = (int)((a.N + per - 1) / per) * a.groups;
   switch (need) {
-    case 1: return launch_form<V, 1, 4>(pass, a, cq, cv, s);
-    case 2: return launch_form<V, 2, 4>(pass, a, cq, cv, s);
-    case 3: return launch_form<V, 3, 4>(pass, a, cq, cv, s);
-    case 4: return launch_form<V, 4, 2>(pass, a, cq, cv, s);
+    case 1: return launch_form<V, 1>(pass, a, cq, cv, s);
+    case 2: return launch_form<V, 2>(pass, a, cq, cv, s);
+    case 3: return launch_form<V, 3>(pass, a, cq, cv, s);
+    case 4: return launch_form<V, 4>(pass, a, cq, cv, s);
     case 5:
-    case 6: return launch_form<V, 6, 1>(pass, a, cq, cv, s);
-    default: return launch_form<V, 8, 1>(pass, a, cq, cv, s);
+    case 6: return launch_form<V, 6>(pass, a, cq, cv, s);
+    default: return launch_form<V, 8>(pass, a, cq, cv, s);
   }
 }
 
