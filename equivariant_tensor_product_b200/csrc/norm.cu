@@ -455,55 +455,72 @@ __global__ void __launch_bounds__(kSumThreads) k_norm_sums(const __grid_constant
   }
 }
 
-// Dropout: a CTA takes a tile of consecutive rows, draws the choices of their channels into
-// shared memory (one generator block for four channels, about 100 instructions) and then passes
-// over the tile's floats, G lanes a row, up to four chunks of a lane in flight.  A table of every
-// float's channel, made once a CTA, stands for the divisions.  Bound by the bytes, 8 a float.
+// Dropout: a warp takes a row, or several narrow ones, at a time, starts reading
+// them, draws the choices of their channels into its part of shared memory meanwhile (one generator
+// block for four channels, about 100 instructions) and applies them, G lanes a row.  A table of every
+// float's channel, made once a CTA, stands for the divisions.  Bound by the bytes, 8 a float: with tiles of
+// rows drawn by a whole CTA between two barriers, a third of the time went to waiting at those (100,000
+// rows of 1,152 floats: 193 us).
 constexpr int kDropThreads = 256;
-constexpr int kDropMaxWords = 4096;    // channels of a tile
+constexpr int kDropWarps = kDropThreads / 32;
+constexpr int kDropAhead = 6;          // chunks of a lane in flight
 
 struct DropoutArgs {
   int64_t N;
-  int dim, C, nb, tile, G;             // rows per tile, lanes per row
+  int dim, C, nb, tile, G;             // rows a warp takes, lanes per row
   int off[kNormMaxBlocks], d[kNormMaxBlocks], coff[kNormMaxBlocks];
   const float* x;
   float* y;
   DropArgs drop;
 };
 
+size_t drop_chan_bytes(int dim) { return (2 * (size_t)dim + 15) & ~(size_t)15; }
+__host__ __device__ inline int drop_words(int tile, int C) { return (tile * C + 3) / 4 + 1; }
+
 template <int V>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(const __grid_constant__ DropoutArgs a) {
   extern __shared__ __align__(16) unsigned char sm[];
   uint16_t* chan = reinterpret_cast<uint16_t*>(sm);
-  uint32_t* words = reinterpret_cast<uint32_t*>(sm + ((2 * (size_t)a.dim + 15) & ~(size_t)15));   // keep bytes, four a word
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // keep bytes, four a word
+  uint32_t* words = reinterpret_cast<uint32_t*>(sm + ((2 * (size_t)a.dim + 15) & ~(size_t)15)) + warp * drop_words(a.tile, a.C);
   for (int i = threadIdx.x; i < a.dim; i += kDropThreads) {
     int b = a.nb - 1;
     while (b > 0 && i < a.off[b]) --b;
     chan[i] = (uint16_t)(a.coff[b] + (i - a.off[b]) / a.d[b]);
   }
   const DropKey key = drop_key(a.drop);
-  const int chunks = a.dim / V, gl = threadIdx.x & (a.G - 1), group = threadIdx.x / a.G, groups = kDropThreads / a.G;
-  for (int64_t t = blockIdx.x; t * a.tile < a.N; t += gridDim.x) {
+  __syncthreads();
+  const int chunks = a.dim / V, gl = lane & (a.G - 1), group = lane / a.G, groups = 32 / a.G;
+  const bool narrow = chunks <= a.G;     // a lane's chunks in flight are those of several rows, not of one
+  const int64_t warps = (int64_t)gridDim.x * kDropWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kDropWarps + warp; t * a.tile < a.N; t += warps) {
     const int64_t row0 = t * a.tile;
     const int rows = (int)min((int64_t)a.tile, a.N - row0);
+    const float* x = a.x + row0 * a.dim;
+    float* y = a.y + row0 * a.dim;
+    bool drawn = false;
     const uint64_t first = (uint64_t)row0 * a.C;
-    const int shift = (int)(first & 3);
-    const int blocks = (rows * a.C + shift + 3) / 4;
-    __syncthreads();
-    for (int i = threadIdx.x; i < blocks; i += kDropThreads) words[i] = keep_bytes(key, a.drop.threshold, (first >> 2) + i);
-    __syncthreads();
-    for (int r = group; r < rows; r += groups) {
-      const unsigned char* keep = reinterpret_cast<const unsigned char*>(words) + shift + r * a.C;
-      const float* x = a.x + (row0 + r) * a.dim;
-      float* y = a.y + (row0 + r) * a.dim;
-      for (int c0 = gl; c0 < chunks; c0 += 4 * a.G) {
-        Chunk<V> v[4];
+    const int shift = (int)(first & 3), blocks = (rows * a.C + shift + 3) / 4;
+    for (int r0 = 0; r0 < rows; r0 += groups * (narrow ? kDropAhead : 1)) {
+      for (int c0 = gl; c0 - gl < chunks; c0 += kDropAhead * a.G) {
+        Chunk<V> v[kDropAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = read_chunk<V>(x + (c0 + i * a.G) * V, c0 + i * a.G < chunks);
+        for (int i = 0; i < kDropAhead; ++i) {
+          const int r = r0 + group + (narrow ? i * groups : 0), c = c0 + (narrow ? 0 : i * a.G);
+          v[i] = read_chunk<V>(x + (int64_t)r * a.dim + c * V, r < rows && c < chunks);
+        }
+        if (!drawn) {
+          drawn = true;
+          __syncwarp();
+          for (int i = lane; i < blocks; i += 32) words[i] = keep_bytes(key, a.drop.threshold, (first >> 2) + i);
+          __syncwarp();
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = c0 + i * a.G;
-          if (c >= chunks) break;
+        for (int i = 0; i < kDropAhead; ++i) {
+          const int r = r0 + group + (narrow ? i * groups : 0), c = c0 + (narrow ? 0 : i * a.G);
+          if (r >= rows || c >= chunks) break;
+          const unsigned char* keep = reinterpret_cast<const unsigned char*>(words) + shift + r * a.C;
           if constexpr (V == 4) {
             const ushort4 u = *reinterpret_cast<const ushort4*>(chan + 4 * c);
             v[i].x[0] = keep[u.x] ? v[i].x[0] * a.drop.inv_keep : 0.0f;
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(kDropThreads) k_dropout(const __grid_constant_
           } else {
             v[i].x[0] = keep[chan[c]] ? v[i].x[0] * a.drop.inv_keep : 0.0f;
           }
-          write_chunk<V>(y + c * V, v[i]);
+          write_chunk<V>(y + (int64_t)r * a.dim + c * V, v[i]);
         }
       }
     }
@@ -854,17 +871,22 @@ tp_status_t tp_dropout_fwd(tp_dropout_t drop, int64_t N, const float* x, double 
   a.N = N;
   a.x = x;
   a.y = y;
-  // tiles of up to 4,096 choices, and no larger than leaves four a SM
-  a.tile = (int)std::max<int64_t>(1, std::min<int64_t>({64, kDropMaxWords / a.C, N / (148 * 4)}));
   const bool vec4 = a.dim % 4 == 0 && al16(x) && al16(y);
   const int chunks = vec4 ? a.dim / 4 : a.dim;
   a.G = 1;
   while (a.G < 32 && a.G < chunks) a.G *= 2;
-  const size_t smem = ((2 * (size_t)a.dim + 15) & ~(size_t)15) + 4 * (((size_t)a.tile * a.C + 3) / 4 + 1);
-  const int64_t tiles = (N + a.tile - 1) / a.tile;
+  // one long row, or rows that give every lane its chunks in flight, and fewer where warps would have none
+  a.tile = chunks > a.G ? 1 : 32 / a.G * kDropAhead;
+  a.tile = (int)std::max<int64_t>(std::min<int64_t>(a.tile, N / (148 * 16)), 1);
+  const size_t smem = drop_chan_bytes(a.dim) + 4 * (size_t)kDropWarps * drop_words(a.tile, a.C);
+  const int64_t tiles = (N + (int64_t)a.tile * kDropWarps - 1) / ((int64_t)a.tile * kDropWarps);
   const unsigned grid = (unsigned)std::min<int64_t>(tiles, 148 * 8);
-  if (vec4) k_dropout<4><<<grid, kDropThreads, smem, s>>>(a);
-  else k_dropout<1><<<grid, kDropThreads, smem, s>>>(a);
+  auto kernel = vec4 ? k_dropout<4> : k_dropout<1>;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e, "tp_dropout");
+  }
+  kernel<<<grid, kDropThreads, smem, s>>>(a);
   count_launches(1);
   return cuda_status(cudaGetLastError(), "tp_dropout");
 }
