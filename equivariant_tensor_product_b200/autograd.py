@@ -211,7 +211,7 @@ def tp_conv_radial(plan: Plan, graph: Graph, x, vec, h, Wr):
 # ---------------------------------------------------------------------------------------------
 
 from .attn import Attention, tp_attn_bwd, tp_attn_fwd  # noqa: E402
-from .block import Dropout, Norm, tp_dropout_bwd, tp_norm_bwd, tp_norm_fwd  # noqa: E402
+from .block import Dropout, Norm, tp_dropout_fwd, tp_norm_bwd, tp_norm_fwd  # noqa: E402
 
 
 def _row_strided(t):
@@ -237,7 +237,11 @@ class AttnFn(torch.autograd.Function):
         q, k, v, table, bucket, rng, y, lse = ctx.saved_tensors
         scale, p, site = ctx.rest
         n = ctx.needs_input_grad
-        colptr, perm = ctx.graph.transpose() if n[1] or n[2] else (None, None)
+        colptr = perm = None
+        # a sender order first made inside a capture would only exist once the capture is replayed: leave it to
+        # the call's workspace then, and the graph object without it
+        if (n[1] or n[2]) and (ctx.graph._colptr is not None or not torch.cuda.is_current_stream_capturing()):
+            colptr, perm = ctx.graph.transpose()
         gq, gk, gv, gtable = tp_attn_bwd(ctx.attn, ctx.graph.rowptr, ctx.graph.src, q, k, v, y, lse, gy.contiguous(),
                                          bucket=bucket, table=table, scale=scale, p=p, rng=rng, site=site,
                                          colptr=colptr, perm=perm, need_gq=n[0], need_gk=n[1], need_gv=n[2],
@@ -249,7 +253,8 @@ def tp_attn(attn: Attention, graph: Graph, q, k, v, bucket=None, table=None, sca
             site: int = 0):
     """y = attention(q, k, v) over the graph's edges with first-order derivatives to q, k, v and table through
     the CUDA kernels.  q, k, v may be column slices of one array.  rng must not change between the forward
-    and the backward call (autograd reports it when it does)."""
+    and the backward call (autograd reports it when it does).  In a CUDA graph capture, run forward and
+    backward in the same capture, by torch.autograd.grad or with no eager graph of the same leaves alive."""
     return AttnFn.apply(q, k, v, table, bucket, rng if p > 0.0 else None, attn, graph, scale, p, site)
 
 
@@ -283,12 +288,12 @@ class DropoutFn(torch.autograd.Function):
     def forward(ctx, x, rng, drop, p, site):
         ctx.save_for_backward(rng)
         ctx.drop, ctx.rest = drop, (p, site)
-        # the forward and backward calls are one linear map and its adjoint, which is the map itself
-        return tp_dropout_bwd(drop, x.contiguous(), p, rng, site)
+        return tp_dropout_fwd(drop, x.contiguous(), p, rng, site)
 
     @staticmethod
     def backward(ctx, gy):
         (rng,) = ctx.saved_tensors
+        # a diagonal map is its own adjoint, so the gradient is differentiable in turn
         return DropoutFn.apply(gy, rng, ctx.drop, *ctx.rest), None, None, None, None
 
 

@@ -747,7 +747,7 @@ __device__ __forceinline__ void table_part(const AttnArgs& a, int cta) {
       }
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (d[i] >= 0 && e0 + i < last) mine[b[i] * a.H] += ds[i];
+        if (d[i] >= 0 && (unsigned)b[i] < (unsigned)a.K && e0 + i < last) mine[b[i] * a.H] += ds[i];
     }
   }
   __syncthreads();
@@ -810,6 +810,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
       if (base + lane < t.hi) {
         e = __ldg(a.perm + base + lane);
         if (e >= e_lo && e < e_hi) i = a.dst[e];
+        if (i >= a.N) i = -1;              // an edge that no row of the row pointers held
       }
       const uint32_t live = __ballot_sync(kFull, i >= 0);
       const int n = __popc(live);

@@ -312,6 +312,29 @@ def test_spare_edges_and_poisoned_buffers(tp):
         tp.tp_attn_bwd(attn, *rows, y, lse, g["gy"], ws=ws[:256], **more)
 
 
+@pytest.mark.parametrize("before", [1, 300, 700])
+def test_spare_edges_before_the_first_row(tp, before):
+    """rowptr[0] > 0: the edges before it belong to no row, next to receivers and senders of very many edges."""
+    rng = np.random.default_rng(20)
+    counts = rng.poisson(6, 40)
+    counts[0], counts[7], counts[39] = 900, 1300, 700
+    rowptr = np.concatenate([[0], np.cumsum(counts)])
+    src = rng.integers(0, 40, rowptr[-1])
+    src[rng.random(len(src)) < 0.4] = 11
+    pr = problem(20, "8x0e+4x1o", "8x0e+4x1o", 4, 40, 0, graph=(rowptr.astype(np.int32), src.astype(np.int32)))
+    want = check(pr, solve(tp, pr))
+    d = pr["d"]
+    d["rowptr"] = (d["rowptr"] + before).astype(np.int32)
+    for name, values in (("src", rng.integers(0, 40, before)), ("bucket", rng.integers(0, 5, before))):
+        d[name] = np.concatenate([values, d[name]]).astype(np.int32)
+    for transposed in (True, False):
+        got = solve(tp, pr, transposed)
+        bound = attn_bounds(pr["qk"], pr["v"], 4, d["rowptr"] - before, d["src"][before:], d["q"], d["k"], d["v"], d["gy"],
+                            want["lse"].numpy(), bucket=d["bucket"][before:], table=d["table"], n_buckets=5, scale=pr["scale"])
+        for name in want:
+            assert_within(got[name], want[name], bound[name], name)
+
+
 def test_graphs_without_edges_or_nodes(tp):
     attn = tp.Attention("8x0e", "8x0e", 2, 5)
     z = lambda *s: torch.zeros(*s, device="cuda")

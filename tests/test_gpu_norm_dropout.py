@@ -308,3 +308,41 @@ def test_a_captured_layer(tp):
     torch.cuda.synchronize()
     eager = step()
     assert all(torch.equal(a, b) for a, b in zip(out, eager))
+
+
+def test_a_layer_captured_before_its_sender_order_exists(tp):
+    """The captured backward builds the order itself and leaves the graph object without it."""
+    P, rowptr, src, vec, x, gy = _make_layer(tp, seed=3)
+    graph = tp.autograd.Graph(dev(rowptr), dev(src))
+    q = torch.randn(40, 40, generator=torch.Generator().manual_seed(4)).cuda().requires_grad_(True)
+    bucket = tp.tp_distance_buckets(dev(vec), P["bounds"], 2.5)
+    step = lambda: torch.autograd.grad(tp.tp_attn(P["attn"], graph, q, q, q, bucket, P["table"]), q, gy)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.no_grad():
+            tp.tp_attn(P["attn"], graph, q, q, q, bucket, P["table"])
+    torch.cuda.current_stream().wait_stream(side)
+    cg = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(cg):
+        out = step()
+    assert graph._colptr is None
+    eager = step()                                             # before the first replay
+    cg.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+
+
+def test_calls_on_another_stream_than_the_current_one(tp):
+    norm, drop = tp.Norm("32x0e+32x1o"), tp.Dropout("32x0e+32x1o")
+    g = torch.Generator("cuda").manual_seed(0)
+    x, gy = (torch.randn(3000, norm.dim, generator=g, device="cuda") for _ in range(2))
+    rng = torch.tensor([1, 2], dtype=torch.int64, device="cuda")
+    want = (tp.tp_norm_fwd(norm, x), *tp.tp_norm_bwd(norm, x, gy), tp.tp_dropout_fwd(drop, x, 0.3, rng))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = (tp.tp_norm_fwd(norm, x, stream=stream), *tp.tp_norm_bwd(norm, x, gy, stream=stream),
+               tp.tp_dropout_fwd(drop, x, 0.3, rng, stream=stream))
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
