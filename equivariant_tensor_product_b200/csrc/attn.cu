@@ -19,7 +19,7 @@
 //
 // Long rows.  A receiver (sender) of more than `hub` edges would keep one warp busy long after the
 // others are done.  Its edges are taken window by window instead: the edge axis is cut into
-// windows of win = hub / 2 edges, one CTA each, behind the CTAs of the rows.  A window meets at
+// windows of win = hub / 2 edges, whose CTAs come before those of the rows.  A window meets at
 // most two such rows (the row of its first edge and the row of its last one), finds them by a
 // 33-way search in the row pointers and leaves a partial row for each; a join kernel adds a row's
 // partials up in window order.  Graphs of at most `hub` edges have neither windows nor the join.
@@ -54,7 +54,7 @@ struct AttnArgs {
   int N, E, H, K;
   int hw, groups;            // heads per warp (a power of two), head groups of a row
   int W;                     // warps that split a row's edges
-  int row_ctas;              // CTAs of the rows; the windows' CTAs come after them
+  int row_ctas, win_ctas;    // CTAs of the rows, and of the windows before them
   int hub, win, n_win;       // rows of more than hub edges go by windows (n_win = 0: no such rows)
   float* part;               // workspace [n_win][2][part_len]: partial rows of the windows
   int part_len;
@@ -84,7 +84,9 @@ struct AttnArgs {
   float2* rec;               // workspace [E][H]: (ds, r p) of the backward pass
   int32_t* dst;              // workspace [E]: receiver, -1 for an edge that takes no part
   float* hist;               // workspace [hist_ctas][K * H]
-  int hist_ctas, hist_copies, hist_lanes;   // hist_ctas = 0 in the sender pass: no table CTAs behind it
+  int hist_ctas, hist_copies, hist_lanes;
+  int table_here;            // sender pass: the table's CTAs come behind it
+  int threads;               // of a CTA of the passes, and of the table's, so that its sums do not depend on where it runs
   HeadMap mq, mv;
 };
 
@@ -117,7 +119,7 @@ __host__ __device__ constexpr int ctas_per_sm(Pass pass, int V, int S) {
   return pass == kRecv ? 4 : 5;
 }
 
-constexpr int kMinWindow = 256;
+constexpr int kMinWindow = 160;
 
 // The kernels of one call follow each other by programmatic dependent launch: a kernel lets the next
 // one be set up from its start on, and the next one waits here, before it touches anything that an
@@ -180,19 +182,24 @@ __device__ __forceinline__ float exp_of(float x) { return exp2f(x * kLog2e); }
 
 __device__ __forceinline__ int clamp_edge(int e, int E) { return min(max(e, 0), E); }
 
-// The row r of `ptr` with ptr[r] <= e < ptr[r + 1], or -1: 32 probes a step, the same answer in every lane.
-__device__ __forceinline__ int find_row(const int32_t* __restrict__ ptr, int N, int e) {
-  if (e < __ldg(ptr) || e >= __ldg(ptr + N)) return -1;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = N;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 32) / 33;
-    const int64_t pos = lo + (int64_t)(lane + 1) * step;
-    const int below = __popc(__ballot_sync(kFull, pos < hi && __ldg(ptr + min(pos, (int64_t)hi)) <= e));
-    lo += below * step;
-    hi = min(hi, lo + step);
+// The rows r of `ptr` with ptr[r] <= e < ptr[r + 1], or -1, for two edges e: 32 probes a step, both
+// searches at once; the same answers in every lane.
+__device__ __forceinline__ void find_rows(const int32_t* __restrict__ ptr, int N, int e0, int e1, int& r0, int& r1) {
+  const int from = __ldg(ptr), to = __ldg(ptr + N), lane = threadIdx.x & 31;
+  int lo[2] = {0, 0}, hi[2] = {N, N};
+  const int e[2] = {e0, e1};
+  while (hi[0] - lo[0] > 1 || hi[1] - lo[1] > 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int step = max((hi[i] - lo[i] + 32) / 33, 1);
+      const int64_t pos = lo[i] + (int64_t)(lane + 1) * step;
+      const int below = __popc(__ballot_sync(kFull, pos < hi[i] && __ldg(ptr + min(pos, (int64_t)hi[i])) <= e[i]));
+      lo[i] += below * step;
+      hi[i] = min(hi[i], lo[i] + step);
+    }
   }
-  return lo;
+  r0 = e0 >= from && e0 < to ? lo[0] : -1;
+  r1 = e1 >= from && e1 < to ? lo[1] : -1;
 }
 
 // A stretch of one row's edges that a CTA's warps work on: a whole row, or a window's share of a long one.
@@ -202,30 +209,30 @@ struct Task {
   bool write;                // false: a long row, which the windows deal with
 };
 
-// The tasks of this CTA.  Rows: one.  Windows: the heads of up to two long rows, found here.
+// The tasks of this CTA.  Rows: one.  Windows: the heads of up to two long rows, found here.  Where a row has
+// one warp, a CTA has no more: with four rows a CTA the warps of the three shorter ones stood idle until
+// the longest was done (1.18M edges with degrees up to 150: 366 us, against 263 with equal degrees).
 template <bool WIDE>
 struct Tasks {
-  int n, next, first, row0, row1;
+  int n, next, window, head_first, row0, row1;
 
   __device__ __forceinline__ Tasks(const AttnArgs& a, const int32_t* __restrict__ ptr) {
-    __shared__ int found[2];
     next = 0;
     n = 1;
-    if ((int)blockIdx.x < a.row_ctas) return;
-    first = ((int)blockIdx.x - a.row_ctas) * a.win;
-    if (threadIdx.x < 64) {
-      const int slot = threadIdx.x >> 5;
-      int r = find_row(ptr, a.N, slot ? min(first + a.win, a.E) - 1 : first);
-      if (r >= 0) {
-        const int start = __ldg(ptr + r);
-        if (__ldg(ptr + r + 1) - start <= a.hub || (slot && start <= first)) r = -1;
-      }
-      if ((threadIdx.x & 31) == 0) found[slot] = r;
+    if ((int)blockIdx.x >= a.win_ctas) return;
+    window = blockIdx.x;
+    head_first = 0;
+    int groups = WIDE ? a.H : a.groups;
+    if (!WIDE && a.W == 1) {             // one head group
+      head_first = window % groups * a.hw;
+      window /= groups;
+      groups = 1;
     }
-    __syncthreads();
-    row0 = found[0];
-    row1 = found[1];
-    n = row0 < 0 && row1 < 0 ? 0 : 2 * (WIDE ? a.H : a.groups);
+    const int first = window * a.win;
+    find_rows(ptr, a.N, first, min(first + a.win, a.E) - 1, row0, row1);
+    if (row0 >= 0 && __ldg(ptr + row0 + 1) - __ldg(ptr + row0) <= a.hub) row0 = -1;
+    if (row1 >= 0 && (__ldg(ptr + row1 + 1) - __ldg(ptr + row1) <= a.hub || __ldg(ptr + row1) <= first)) row1 = -1;
+    n = row0 < 0 && row1 < 0 ? 0 : 2 * groups;
   }
 
   __device__ __forceinline__ bool get(const AttnArgs& a, const int32_t* __restrict__ ptr, Task& t) {
@@ -235,18 +242,19 @@ struct Tasks {
     t.write = false;
     t.lo = t.hi = t.split = 0;
     t.W = 1;
-    if ((int)blockIdx.x < a.row_ctas) {
+    if ((int)blockIdx.x >= a.win_ctas) {
+      const int cta = (int)blockIdx.x - a.win_ctas;
       next = 1;
       if (WIDE) {
-        t.row = blockIdx.x / a.H;
-        t.head0 = blockIdx.x - t.row * a.H;
+        t.row = cta / a.H;
+        t.head0 = cta - t.row * a.H;
       } else {
         // one head group after the other: what a group reads of k and v stays in L2 for longer
-        const int blocks = a.row_ctas / a.groups, g = blockIdx.x / blocks;
+        const int blocks = a.row_ctas / a.groups, g = cta / blocks;
         t.head0 = g * a.hw;
         t.W = a.W;
         t.split = warp % a.W;
-        t.row = ((int)blockIdx.x - g * blocks) * (kAttnWarps / a.W) + warp / a.W;
+        t.row = (cta - g * blocks) * ((int)(blockDim.x >> 5) / a.W) + warp / a.W;
         if (t.row >= a.N) return true;
       }
       t.lo = clamp_edge(__ldg(ptr + t.row), a.E);
@@ -254,18 +262,18 @@ struct Tasks {
       t.write = a.n_win == 0 || t.hi - t.lo <= a.hub;
       if (!t.write) t.hi = t.lo;
     } else {
-      const int per = WIDE ? a.H : a.groups, slot = next / per;
+      const int per = n / 2, slot = next / per, first = window * a.win;
       if (next > 0) __syncthreads();     // the join buffer is free again
       t.row = slot ? row1 : row0;
-      t.head0 = (next - slot * per) * (WIDE ? 1 : a.hw);
+      t.head0 = head_first + (next - slot * per) * (WIDE ? 1 : a.hw);
       ++next;
       if (t.row < 0) return true;
       t.write = true;
-      t.part = a.part + ((int64_t)((int)blockIdx.x - a.row_ctas) * 2 + slot) * a.part_len;
+      t.part = a.part + ((int64_t)window * 2 + slot) * a.part_len;
       t.lo = max(__ldg(ptr + t.row), first);
       t.hi = min(min(__ldg(ptr + t.row + 1), first + a.win), a.E);
       if (!WIDE) {
-        t.W = kAttnWarps;
+        t.W = blockDim.x >> 5;
         t.split = warp;
       }
     }
@@ -384,6 +392,16 @@ __device__ __forceinline__ Batch batch_of_warp(int hw) {
   int* p = reinterpret_cast<int*>(dyn) + (threadIdx.x >> 5) * (96 + 64 * hw);
   return Batch{p, p + 32, reinterpret_cast<uint32_t*>(p + 64), reinterpret_cast<float*>(p + 96)};
 }
+// Behind the warps' batches: where the warps of a row, or of a WIDE row's dot products, meet.
+__device__ __forceinline__ float* join_of_cta(int hw) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  return reinterpret_cast<float*>(dyn) + (blockDim.x >> 5) * (96 + 64 * hw);
+}
+// Floats of it for a pass: two turns of the dot products, or a warp's partial row for every warp.
+constexpr int join_floats(Pass pass, int V, int SQ, int SV, bool wide, int u) {
+  if (wide) return pass == kSend ? 0 : 2 * (kAttnWideThreads / 32) * (pass == kRecv ? 2 : 1) * u;
+  return kAttnWarps * 32 * (pass == kFwd ? V * SV + 2 : pass == kRecv ? V * SQ : V * (SQ + SV));
+}
 size_t batch_bytes(int threads, int hw) { return (size_t)(threads / 32) * (96 + 64 * hw) * 4; }
 
 // An entry whose table value is -inf: its edge takes no part for that head, and no row of it may reach
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
   constexpr int U = rows_at_once(kFwd, V, SV, WIDE);
   // rows of k at a time: more where a lane holds but one chunk of them
   constexpr int UA = WIDE ? U : SQ == 1 || (SQ == 2 && V == 1) ? 8 : SQ == 2 ? 4 : U;
-  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * U : kAttnWarps * (V * SV + 2) * 32];
+  float* const join = join_of_cta(a.hw);
   let_next_launch();
   const int lane = threadIdx.x & 31;
   const Batch B = batch_of_warp(a.hw);
@@ -571,7 +589,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
 template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kRecv, V, SV)) k_attn_bwd_recv(const __grid_constant__ AttnArgs a) {
   constexpr int U = rows_at_once(kRecv, V, SV, WIDE);
-  __shared__ float join[WIDE ? 2 * (kAttnWideThreads / 32) * 2 * U : kAttnWarps * V * SQ * 32];
+  float* const join = join_of_cta(a.hw);
   let_next_launch();
   const int lane = threadIdx.x & 31;
   const Batch B = batch_of_warp(a.hw);
@@ -758,7 +776,7 @@ __device__ __forceinline__ void table_part(const AttnArgs& a, int cta) {
   }
 }
 
-__global__ void __launch_bounds__(kAttnThreads) k_attn_table(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kAttnWideThreads) k_attn_table(const __grid_constant__ AttnArgs a) {
   let_next_launch();
   table_part(a, blockIdx.x);
 }
@@ -780,11 +798,11 @@ __device__ __forceinline__ void table_sum(const AttnArgs& a, int o) {
 template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kSend, V, SV)) k_attn_bwd_send(const __grid_constant__ AttnArgs a) {
   constexpr int U = rows_at_once(kSend, V, SV, WIDE);
-  __shared__ float join[WIDE ? 1 : kAttnWarps * V * (SQ + SV) * 32];
+  float* const join = join_of_cta(a.hw);
   let_next_launch();
-  if ((int)blockIdx.x >= a.row_ctas + a.n_win) {
+  if ((int)blockIdx.x >= a.row_ctas + a.win_ctas) {
     wait_for_previous();
-    table_part(a, (int)blockIdx.x - a.row_ctas - a.n_win);
+    table_part(a, (int)blockIdx.x - a.row_ctas - a.win_ctas);
     return;
   }
   const int lane = threadIdx.x & 31;
@@ -922,7 +940,8 @@ __device__ __forceinline__ void join_long_row(const AttnArgs& a, int w, const fl
   const int32_t* ptr = PASS == 2 ? a.colptr : a.rowptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32;
   const int first = w * a.win, end = min(first + a.win, a.E);
-  const int row = find_row(ptr, a.N, end - 1);   // the row pointers are the caller's: read before the wait
+  int row, same;
+  find_rows(ptr, a.N, end - 1, end - 1, row, same);   // the row pointers are the caller's: read before the wait
   wait_for_previous();
   if (row < 0) return;
   const int start = __ldg(ptr + row), stop = min(__ldg(ptr + row + 1), a.E);
@@ -1123,17 +1142,35 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
+// Copies of the table per CTA: one per group of lanes while they fit 32 KB, at least one.  CTAs: enough that a
+// group has no more than some 48 edges, as long as a CTA has as many edges' values as it zeroes, sums
+// and writes floats.
+void hist_plan(AttnArgs& a, int threads) {
+  a.hist_lanes = 1;
+  while (a.hist_lanes < a.H) a.hist_lanes *= 2;
+  const int KH = std::max(1, a.K * a.H);
+  a.hist_copies = std::max(1, std::min(threads / a.hist_lanes, 8 * 1024 / KH));
+  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(a.hist_copies * 48, KH / a.H * 4));
+  a.hist_ctas = (int)std::min<int64_t>(want, 148 * 2 * (kAttnThreads / std::min(threads, kAttnThreads)));
+}
+
 // Shared memory of a table_part CTA.
 size_t hist_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H * a.hist_copies; }
 
+// The table's CTAs behind the sender pass's, with as many threads.
+void plan_table(AttnArgs& a, int threads) {
+  a.threads = threads;
+  if (a.table_here) hist_plan(a, threads);
+}
+
 template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
 cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s) {
-  // more than 48 KB with the kernel's own arrays (the largest: 17 KB) has to be asked for
-  auto allow = [](auto kernel, size_t smem) {
-    return smem <= 30 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto allow = [](auto kernel, size_t smem) {            // beyond 48 KB it has to be asked for
+    return smem <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   };
   size_t smem = batch_bytes(threads, a.hw);
-  const unsigned grid = (unsigned)(a.row_ctas + a.n_win);
+  if (WIDE || a.W > 1) smem += sizeof(float) * join_floats(pass, V, SQ, SV, WIDE, rows_at_once(pass, V, SV, WIDE));
+  const unsigned grid = (unsigned)(a.row_ctas + a.win_ctas);
   if (pass == kSend) {
     if (a.hist_ctas > 0) smem = std::max(smem, hist_bytes(a));
     cudaError_t e = allow(k_attn_bwd_send<V, SQ, SV, LOOSE, WIDE>, smem);
@@ -1158,13 +1195,13 @@ cudaError_t launch_form(Pass pass, const AttnArgs& a, int cq, int cv, cudaStream
   const int G = 32 / a.hw;
   auto fills = [G](int chunks, int slots) { return chunks >= (slots - 1) * G && chunks <= slots * G; };
   if (fills(cv, S)) {
-    if (fills(cq, 1)) return launch_one<V, 1, S, false, false>(pass, a, kAttnThreads, s);
+    if (fills(cq, 1)) return launch_one<V, 1, S, false, false>(pass, a, a.W == 1 ? 32 : kAttnThreads, s);
     if constexpr (S > 2) {
-      if (fills(cq, 2)) return launch_one<V, 2, S, false, false>(pass, a, kAttnThreads, s);
+      if (fills(cq, 2)) return launch_one<V, 2, S, false, false>(pass, a, a.W == 1 ? 32 : kAttnThreads, s);
     }
-    if (fills(cq, S)) return launch_one<V, S, S, false, false>(pass, a, kAttnThreads, s);
+    if (fills(cq, S)) return launch_one<V, S, S, false, false>(pass, a, a.W == 1 ? 32 : kAttnThreads, s);
   }
-  return launch_one<V, S, S, true, false>(pass, a, kAttnThreads, s);
+  return launch_one<V, S, S, true, false>(pass, a, a.W == 1 ? 32 : kAttnThreads, s);
 }
 
 template <int V>
@@ -1177,6 +1214,8 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
     a.groups = a.H;
     a.W = 1;
     a.row_ctas = a.N * a.H;
+    a.win_ctas = a.n_win;
+    plan_table(a, threads);
     if (chunks <= 4 * threads) return launch_one<V, 4, 4, true, true>(pass, a, threads, s);
     return launch_one<V, 8, 8, true, true>(pass, a, threads, s);
   }
@@ -1189,8 +1228,10 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)a.N * a.groups;
   a.W = 1;
   while (a.W < kAttnWarps && units * a.W < 148 * 8 && a.E / std::max(1, a.N) >= 8 * a.W) a.W *= 2;
-  const int per = kAttnWarps / a.W;
+  const int per = a.W == 1 ? 1 : kAttnWarps / a.W;
   a.row_ctas = (int)((a.N + per - 1) / per) * a.groups;
+  a.win_ctas = a.n_win * (a.W == 1 ? a.groups : 1);
+  plan_table(a, a.W == 1 ? 32 : kAttnThreads);
   switch (need) {
     case 1: return launch_form<V, 1>(pass, a, cq, cv, s);
     case 2: return launch_form<V, 2>(pass, a, cq, cv, s);
@@ -1202,8 +1243,10 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   }
 }
 
-// Windows of at least 128 edges, and no more of them than 16 a SM: rows of up to twice that stay with
-// their own warps.
+// Windows of at least 160 edges, and no more of them than 16 a SM: rows of up to twice that stay with their own
+// warps.  Fewer CTAs that look for long rows in vain against shorter ones for those there are: with 128 / 160 /
+// 192 / 256 edges 162,892 edges without a long row take 213 / 210 / 208 / 208 us backward, 311,027 edges with a
+// node of 8,192 neighbours 225 / 225 / 236 / 253.
 void window_plan(AttnArgs& a) {
   a.win = std::max(kMinWindow, (a.E / (148 * 16) + 32) / 32 * 32);
   a.hub = 2 * a.win;
@@ -1221,17 +1264,6 @@ cudaError_t launch_pass(Pass pass, AttnArgs& a, bool vec4, float* part, cudaStre
   a.part = part;
   a.part_len = part_len(a, pass);
   return vec4 ? launch_slots<4>(pass, a, s) : launch_slots<1>(pass, a, s);
-}
-
-// Copies of the table per CTA: one per group of lanes while they fit 32 KB, at least one.
-void hist_plan(AttnArgs& a) {
-  a.hist_lanes = 1;
-  while (a.hist_lanes < a.H) a.hist_lanes *= 2;
-  const int KH = std::max(1, a.K * a.H);
-  a.hist_copies = std::max(1, std::min(kAttnThreads / a.hist_lanes, 8 * 1024 / KH));
-  // a CTA zeroes, sums and writes KH floats: give it at least as many edges' values
-  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(a.hist_copies * 16, KH / a.H * 4));
-  a.hist_ctas = (int)std::min<int64_t>(want, 148 * 2);
 }
 
 }  // namespace
@@ -1254,8 +1286,12 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   AttnArgs a = h->proto;
   a.N = (int)N;
   a.E = (int)E;
-  hist_plan(a);
   window_plan(a);
+  int hist_ctas = 0;         // whatever the threads of the sender pass will be
+  for (int threads : {32, kAttnThreads, kAttnWideThreads}) {
+    hist_plan(a, threads);
+    hist_ctas = std::max(hist_ctas, a.hist_ctas);
+  }
   BwdLayout L;
   size_t off = 0;
   const size_t e = (size_t)std::max<int64_t>(E, 1);
@@ -1264,7 +1300,7 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   L.dst = off;
   off += al256(sizeof(int32_t) * e);
   L.hist = off;
-  off += al256(sizeof(float) * (size_t)a.hist_ctas * a.K * a.H);
+  off += al256(sizeof(float) * (size_t)hist_ctas * a.K * a.H);
   L.colptr = off;
   off += al256(sizeof(int32_t) * (size_t)(N + 1));
   L.perm = off;
@@ -1508,29 +1544,25 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   tail.send_len = part_len(a, kSend);
   tail.recv_joins = gq ? a.n_win : 0;
   tail.send_joins = send ? a.n_win : 0;
-  AttnArgs hist = a;
-  hist.hist_ctas = 0;
-  if (gtable && E > 0) hist_plan(hist);
-  // the table's CTAs run behind the sender pass's where their shared memory leaves those their place
-  const bool fused = send && hist.hist_ctas > 0 && hist_bytes(hist) <= 32 * 1024;
-  a.hist_ctas = fused ? hist.hist_ctas : 0;
-  a.hist_copies = hist.hist_copies;
-  a.hist_lanes = hist.hist_lanes;
+  // behind the sender pass while a copy of the table leaves that pass's CTAs their shared memory
+  a.table_here = gtable && E > 0 && send && (size_t)a.K * a.H * sizeof(float) <= 32 * 1024;
+  a.hist_ctas = 0;
   e = launch_pass(kRecv, a, vec4, tail.recv_part, s);
+  a.hist_ctas = 0;
   if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, tail.send_part, s);
-  if (e == cudaSuccess && hist.hist_ctas > 0 && !fused) {
-    const size_t smem = hist_bytes(hist);
+  if (e == cudaSuccess && gtable && E > 0 && !a.table_here) {
+    hist_plan(a, a.threads);
+    const size_t smem = hist_bytes(a);
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_attn_table, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     // an ordinary launch: set up early, its few CTAs would gather on the SMs that the receiver pass leaves
     // first and run there one after another (162,892 edges: 46 instead of 16 us)
     if (e == cudaSuccess) {
-      k_attn_table<<<hist.hist_ctas, kAttnThreads, smem, s>>>(hist);
+      k_attn_table<<<a.hist_ctas, a.threads, smem, s>>>(a);
       count_launches(1);
       e = cudaGetLastError();
     }
   }
-  a.hist_ctas = hist.hist_ctas;
-  const int sums = hist.hist_ctas > 1 ? (a.K * a.H + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
+  const int sums = a.hist_ctas > 1 ? (a.K * a.H + kJoinThreads / 32 - 1) / (kJoinThreads / 32) : 0;
   const unsigned rest = (unsigned)(tail.recv_joins + tail.send_joins + sums);
   if (e == cudaSuccess && rest > 0) e = launch_after(k_attn_bwd_tail, rest, kJoinThreads, 0, s, a, tail);
   return cuda_status(e, "tp_attn_bwd");
