@@ -346,3 +346,34 @@ def test_calls_on_another_stream_than_the_current_one(tp):
                tp.tp_dropout_fwd(drop, x, 0.3, rng, stream=stream))
         s.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_no_device_memory_with_buffers_given(tp):
+    """With outputs and workspaces given, no call allocates."""
+    P, rowptr, src, vec, x, gy = _make_layer(tp, seed=5)
+    N, E = 40, len(src)
+    rowptr, src, vec = dev(rowptr), dev(src), dev(vec)
+    new = lambda *s: torch.empty(*s, device="cuda")
+    byte = lambda n: torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+    rng = torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+    attn, norm, drop = P["attn"], P["norm"], P["drop"]
+    ws_f, ws_b = byte(tp.tp_attn_workspace_size(attn, N, E, 0)), byte(tp.tp_attn_workspace_size(attn, N, E, 1))
+    ws_n = byte(tp.tp_norm_workspace_size(norm, N, 1))
+    bucket, y, lse, z = torch.empty(E, dtype=torch.int32, device="cuda"), new(N, 40), new(N, HEADS), new(N, 40)
+    gq, gk, gv, gt, gw, gb = new(N, 40), new(N, 40), new(N, 40), new(K, HEADS), new(24), new(16)
+
+    def step():
+        tp.tp_distance_buckets(vec, P["bounds"], 2.5, bucket=bucket)
+        tp.tp_norm_fwd(norm, x, P["weight"], P["bias"], y=z)
+        more = dict(bucket=bucket, table=P["table"], p=0.2, rng=rng)
+        tp.tp_attn_fwd(attn, rowptr, src, z, z, z, y=y, lse=lse, ws=ws_f, **more)
+        tp.tp_attn_bwd(attn, rowptr, src, z, z, z, y, lse, gy, gq=gq, gk=gk, gv=gv, gtable=gt, ws=ws_b, **more)
+        tp.tp_norm_bwd(norm, x, gq, P["weight"], gx=gq, gweight=gw, gbias=gb, ws=ws_n)
+        tp.tp_dropout_fwd(drop, y, 0.2, rng, y=y)
+    step()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before, free = torch.cuda.memory_allocated(), torch.cuda.mem_get_info()[0]
+    step()
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() == before and torch.cuda.mem_get_info()[0] == free
