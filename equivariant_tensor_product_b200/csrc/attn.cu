@@ -1,7 +1,7 @@
 // Equivariant neighbour attention (include/tp_attn.h): softmax over each receiver's edges, with a
 // bias per distance bucket and dropout of the probabilities, and its backward pass.
 //
-// Mapping.  A head's floats (its part of every irreps block) are cut into chunks of V = 4 (or 1)
+// Mapping.  A head's floats (its part of every irreps block) are cut into chunks of V = 4 (2, 1)
 // floats and dealt to a group of G lanes, S chunks a lane, so that a lane's chunks of q, of the
 // accumulators and of the gathered rows stay in registers and a dot product ends in log2 G
 // shuffles.  A warp holds 32 / G heads of one receiver; heads beyond 1,024 floats take a whole
@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -106,7 +107,7 @@ enum Pass { kFwd, kRecv, kSend };
 // U 2 at 5 47, U 4 at 5 53; sender U 2 at 6 33, at 5 37.
 __host__ __device__ constexpr int rows_at_once(Pass pass, int V, int S, bool wide) {
   if (wide) return S <= 4 ? 2 : 1;
-  if (V == 1) return S <= 3 || (S == 4 && pass == kFwd) ? 4 : S == 4 || pass != kRecv ? 2 : 1;
+  if (V < 4) return S <= 3 || (S == 4 && pass == kFwd) ? 4 : S == 4 || pass != kRecv ? 2 : 1;
   if (S <= 2) return 4;
   if (S == 3) return pass == kRecv ? 2 : 4;
   return S == 4 && pass != kSend ? 2 : 1;
@@ -114,6 +115,7 @@ __host__ __device__ constexpr int rows_at_once(Pass pass, int V, int S, bool wid
 __host__ __device__ constexpr int ctas_per_sm(Pass pass, int V, int S) {
   if (S >= 6) return S == 6 ? 3 : 2;
   if (V == 1) return pass == kSend ? 6 : 5;
+  if (V == 2) return pass == kRecv ? 4 : 5;
   if (S <= 2) return 4;
   if (S == 3) return pass == kSend ? 3 : 4;
   return pass == kRecv ? 4 : 5;
@@ -157,6 +159,9 @@ __device__ __forceinline__ Vec<V> load_vec(const char* p, bool on) {
     if constexpr (V == 4) {
       const float4 t = __ldg(reinterpret_cast<const float4*>(p));
       r.x[0] = t.x, r.x[1] = t.y, r.x[2] = t.z, r.x[3] = t.w;
+    } else if constexpr (V == 2) {
+      const float2 t = __ldg(reinterpret_cast<const float2*>(p));
+      r.x[0] = t.x, r.x[1] = t.y;
     } else {
       r.x[0] = __ldg(reinterpret_cast<const float*>(p));
     }
@@ -173,6 +178,8 @@ template <int V>
 __device__ __forceinline__ void store_vec(float* p, const Vec<V>& r) {
   if constexpr (V == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(r.x[0], r.x[1], r.x[2], r.x[3]);
+  } else if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(r.x[0], r.x[1]);
   } else {
     *p = r.x[0];
   }
@@ -412,7 +419,7 @@ template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ? 1 : ctas_per_sm(kFwd, V, SV)) k_attn_fwd(const __grid_constant__ AttnArgs a) {
   constexpr int U = rows_at_once(kFwd, V, SV, WIDE);
   // rows of k at a time: more where a lane holds but one chunk of them
-  constexpr int UA = WIDE ? U : SQ == 1 || (SQ == 2 && V == 1) ? 8 : SQ == 2 ? 4 : U;
+  constexpr int UA = WIDE ? U : SQ == 1 || (SQ == 2 && V < 4) ? 8 : SQ == 2 ? 4 : U;
   float* const join = join_of_cta(a.hw);
   let_next_launch();
   const int lane = threadIdx.x & 31;
@@ -1260,10 +1267,12 @@ int part_len(const AttnArgs& a, Pass pass) {
 
 size_t part_bytes(const AttnArgs& a, Pass pass) { return sizeof(float) * 2 * (size_t)a.n_win * part_len(a, pass); }
 
-cudaError_t launch_pass(Pass pass, AttnArgs& a, bool vec4, float* part, cudaStream_t s) {
+// width: floats of a chunk.
+cudaError_t launch_pass(Pass pass, AttnArgs& a, int width, float* part, cudaStream_t s) {
   a.part = part;
   a.part_len = part_len(a, pass);
-  return vec4 ? launch_slots<4>(pass, a, s) : launch_slots<1>(pass, a, s);
+  if (width == 4) return launch_slots<4>(pass, a, s);
+  return width == 2 ? launch_slots<2>(pass, a, s) : launch_slots<1>(pass, a, s);
 }
 
 }  // namespace
@@ -1273,7 +1282,7 @@ using namespace tp;
 
 struct tp_attn_s {
   AttnArgs proto;
-  bool vec4;                 // every head's floats of every block are a multiple of four
+  int width;                 // the largest of 4, 2, 1 that divides every head's floats of every block
 };
 
 namespace {
@@ -1360,8 +1369,13 @@ tp_status_t attn_inputs(tp_attn_t h, int64_t N, int64_t E, const int32_t* rowptr
   return TP_OK;
 }
 
-bool rows4(const AttnArgs& a) {
-  return al16(a.q) && al16(a.k) && al16(a.v) && a.ldq % 16 == 0 && a.ldk % 16 == 0 && a.ldv % 16 == 0;
+// The widest chunk, up to `width` floats, that pointers and row strides (in floats) allow.
+int chunk_width(int width, std::initializer_list<const void*> pointers, std::initializer_list<int64_t> strides) {
+  for (const void* p : pointers)
+    while (reinterpret_cast<uintptr_t>(p) % (4 * width) != 0) width /= 2;
+  for (int64_t ld : strides)
+    while (ld % width != 0) width /= 2;
+  return width;
 }
 
 bool head_map(const std::vector<IrrepTerm>& t, int heads, HeadMap& m, int& dim) {
@@ -1394,7 +1408,7 @@ tp_status_t tp_attn_create(tp_attn_t* attn, const char* irreps_qk, const char* i
     return set_failure(TP_ERR_UNSUPPORTED, "at most 4096 buckets and 32768 table entries");
   tp_attn_s h;
   std::memset(&h, 0, sizeof(h));
-  h.vec4 = true;
+  h.width = 4;
   struct Side {
     const char* irreps;
     const char* name;
@@ -1416,7 +1430,8 @@ tp_status_t tp_attn_create(tp_attn_t* attn, const char* irreps_qk, const char* i
     if (width > (int64_t)4096 * heads) return set_failure(TP_ERR_UNSUPPORTED, "a head has at most 4096 floats");
     if (!head_map(t, heads, *side.map, *side.dim))
       return set_failure(TP_ERR_INVALID_ARG, std::string(side.name) + ": heads must divide every multiplicity");
-    for (int b = 0; b < side.map->nb; ++b) h.vec4 = h.vec4 && side.map->len[b] % 4 == 0;
+    for (int b = 0; b < side.map->nb; ++b)
+      while (side.map->len[b] % h.width != 0) h.width /= 2;
   }
   h.proto.H = heads;
   h.proto.K = n_buckets;
@@ -1469,7 +1484,8 @@ tp_status_t tp_attn_fwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   a.y = y;
   a.lse = lse;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pass(kFwd, a, attn->vec4 && rows4(a) && al16(y), static_cast<float*>(ws), s);
+  const int width = chunk_width(attn->width, {q, k, v, y}, {ldq, ldk, ldv});
+  cudaError_t e = launch_pass(kFwd, a, width, static_cast<float*>(ws), s);
   if (e == cudaSuccess && a.n_win > 0) e = launch_after(k_attn_fwd_join, (unsigned)a.n_win, kJoinThreads, 0, s, a);
   return cuda_status(e, "tp_attn_fwd");
 }
@@ -1535,8 +1551,8 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   a.rec = send || gtable ? reinterpret_cast<float2*>(w + L.rec) : nullptr;
   a.dst = reinterpret_cast<int32_t*>(w + L.dst);
   a.hist = reinterpret_cast<float*>(w + L.hist);
-  const bool vec4 = attn->vec4 && rows4(a) && al16(y) && al16(gy) && al16(gq) && al16(gk) && al16(gv) &&
-                    (!gq || ldgq % 4 == 0) && (!gk || ldgk % 4 == 0) && (!gv || ldgv % 4 == 0);
+  const int width = chunk_width(attn->width, {q, k, v, y, gy, gq, gk, gv},
+                                {ldq, ldk, ldv, gq ? ldgq : 0, gk ? ldgk : 0, gv ? ldgv : 0});
   Tail tail{};
   tail.recv_part = reinterpret_cast<float*>(w + L.recv_part);
   tail.send_part = reinterpret_cast<float*>(w + L.send_part);
@@ -1547,9 +1563,9 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   // behind the sender pass while a copy of the table leaves that pass's CTAs their shared memory
   a.table_here = gtable && E > 0 && send && (size_t)a.K * a.H * sizeof(float) <= 32 * 1024;
   a.hist_ctas = 0;
-  e = launch_pass(kRecv, a, vec4, tail.recv_part, s);
+  e = launch_pass(kRecv, a, width, tail.recv_part, s);
   a.hist_ctas = 0;
-  if (e == cudaSuccess && send) e = launch_pass(kSend, a, vec4, tail.send_part, s);
+  if (e == cudaSuccess && send) e = launch_pass(kSend, a, width, tail.send_part, s);
   if (e == cudaSuccess && gtable && E > 0 && !a.table_here) {
     hist_plan(a, a.threads);
     const size_t smem = hist_bytes(a);

@@ -43,9 +43,10 @@
  *
  * Ownership, streams and errors as in tp.h; the library owns only the handle (host memory).
  * Calls on one handle from several threads or streams are independent as long as their
- * workspaces are.  Pointers need 4-byte alignment; when every pointer is 16-byte aligned and
- * every width (a head's floats in each block) and ld is a multiple of 4, rows move 16 bytes
- * at a time.  The workspace needs 256-byte alignment.
+ * workspaces are.  Pointers need 4-byte alignment; when every pointer is 16-byte (8-byte)
+ * aligned and every width (a head's floats in each block) and ld is a multiple of 4 (2), rows
+ * move 16 (8) bytes at a time, else 4.  The workspace needs 256-byte alignment.  Row strides
+ * stay below 2^30 floats, E and N * heads below 2^31 - 2^22.
  */
 #ifndef TP_ATTN_H_
 #define TP_ATTN_H_
@@ -68,7 +69,7 @@ tp_status_t tp_attn_destroy(tp_attn_t attn);
 tp_status_t tp_attn_query(tp_attn_t attn, int64_t* qk_dim, int64_t* v_dim);
 
 /* Device workspace bytes of a call of kind op (TP_OP_FWD or TP_OP_BWD) for N nodes and E edges.
- * Forward: partial rows of receivers with very many edges (0 for E <= 256), node-sized in all.
+ * Forward: partial rows of receivers with very many edges (0 for E <= 320), node-sized in all.
  * Backward: those, two floats per edge and head, the receiver of each edge, partials of gtable,
  * and room for the transpose. */
 tp_status_t tp_attn_workspace_size(tp_attn_t attn, int64_t N, int64_t E, int32_t op, size_t* bytes);
