@@ -649,11 +649,21 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
       }
       __syncwarp();
       bool any_out = false;              // bias and dropout factor, one lane per edge and head
-      for (int i = L.first(); i < n; i += L.step()) {
-        const float bias = a.table && L.live ? __ldg(a.table + (int64_t)B.b[i] * a.H + L.h) : 0.0f;
-        const bool out = bias == -INFINITY || lse == -INFINITY;
-        any_out |= out;
-        w2[i * a.hw + L.sub] = make_float2(out ? -INFINITY : bias - lse, (B.c[i] >> L.sub) & 1u ? a.drop.inv_keep : 0.0f);
+      for (int i0 = L.first(); i0 < n; i0 += 4 * L.step()) {
+        float bias[4];                   // four reads at a time
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * L.step();
+          bias[k] = a.table && L.live && i < n ? __ldg(a.table + (int64_t)B.b[i] * a.H + L.h) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + k * L.step();
+          if (i >= n) break;
+          const bool out = bias[k] == -INFINITY || lse == -INFINITY;
+          any_out |= out;
+          w2[i * a.hw + L.sub] = make_float2(out ? -INFINITY : bias[k] - lse, (B.c[i] >> L.sub) & 1u ? a.drop.inv_keep : 0.0f);
+        }
       }
       any_out = __any_sync(kFull, any_out);
       __syncwarp();
@@ -848,10 +858,20 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
       }
       __syncwarp();
       bool any_out = false;
-      for (int c = L.first(); c < n; c += L.step()) {
-        const float2 w = L.live ? a.rec[(int64_t)B.b[c] * a.H + L.h] : make_float2(0.0f, 0.0f);
-        any_out |= marked(w.y);
-        w2[c * a.hw + L.sub] = w;
+      for (int c0 = L.first(); c0 < n; c0 += 4 * L.step()) {
+        float2 w[4];                     // four reads at a time
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + k * L.step();
+          w[k] = L.live && c < n ? a.rec[(int64_t)B.b[c] * a.H + L.h] : make_float2(0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + k * L.step();
+          if (c >= n) break;
+          any_out |= marked(w[k].y);
+          w2[c * a.hw + L.sub] = w[k];
+        }
       }
       any_out = __any_sync(kFull, any_out);
       __syncwarp();
