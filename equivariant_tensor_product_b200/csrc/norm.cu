@@ -2,8 +2,8 @@
 //
 // Norm.  The blocks of a row are independent, so each is a short row of its own: a CTA works on one
 // block of many rows.  A block's floats are read once and kept in registers: its chunks of V floats
-// (4, or 1 where a length or a pointer does not allow 16 bytes) are dealt to a group of G lanes, S
-// chunks a lane, several rows a warp where they are few.  A sum over the block is log2 G shuffles;
+// (4, or 2 or 1 where a length or a pointer does not allow 16 or 8 bytes) are dealt to a group of G lanes,
+// S chunks a lane, several rows a warp where they are few.  A sum over the block is log2 G shuffles;
 // mean first, then the square of what is left of it, both from registers instead of one pass with a
 // difference of large sums.  The backward pass keeps every lane's sums of gy n and gy in registers
 // over all rows of the lane, adds them up per CTA, and a second kernel adds the CTAs, so gweight and
@@ -12,7 +12,9 @@
 // Bound by the bytes (8 a float forward, 12 backward) as long as the instructions keep up, which is
 // why a block and not a row is the unit: with whole rows a warp (9 chunks a lane at 1,152 floats) the
 // sums over three blocks, each chunk asking which one it belongs to, took 365 us for 100,000 rows
-// backward, and with whole rows a CTA, through shared memory, 886 us.
+// backward, and with whole rows a CTA, through shared memory, 886 us.  8-byte chunks for even lengths:
+// 18,262 rows of five blocks of 78 channels went from 78 to 47 us forward and 213 to 102 backward against
+// single floats.
 //
 // Blocks of more than 1,152 floats take one CTA per row with three reads of the row, the later ones
 // from L1: k_norm_any.
@@ -75,6 +77,9 @@ __device__ __forceinline__ Chunk<V> read_chunk(const float* p, bool on) {
     if constexpr (V == 4) {
       const float4 t = *reinterpret_cast<const float4*>(p);
       r.x[0] = t.x, r.x[1] = t.y, r.x[2] = t.z, r.x[3] = t.w;
+    } else if constexpr (V == 2) {
+      const float2 t = *reinterpret_cast<const float2*>(p);
+      r.x[0] = t.x, r.x[1] = t.y;
     } else {
       r.x[0] = *p;
     }
@@ -85,6 +90,7 @@ __device__ __forceinline__ Chunk<V> read_chunk(const float* p, bool on) {
 template <int V>
 __device__ __forceinline__ void write_chunk(float* p, const Chunk<V>& r) {
   if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(r.x[0], r.x[1], r.x[2], r.x[3]);
+  else if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(r.x[0], r.x[1]);
   else *p = r.x[0];
 }
 
@@ -153,15 +159,16 @@ struct RowLanes {
   }
 };
 
-// Rows in flight a group: about four chunks (V = 4) or eight floats a lane on their way.
-template <int V, int S>
-struct RowsAtOnce {
-  static constexpr int value = V == 4 ? (S == 1 ? 4 : S == 2 ? 2 : 1) : (S <= 2 ? 4 : S <= 4 ? 2 : 1);
-};
+// Rows in flight a group: up to 16 floats a lane on their way, 8 with single floats, whose addresses and
+// limits take as many registers as their data (311,042 rows of 21 channels, four blocks, backward: 579 us
+// with 8 floats in flight, 622 with 16, which spill).
+__host__ __device__ constexpr int rows_in_flight(int V, int S) {
+  return V == 4 ? (S == 1 ? 4 : S == 2 ? 2 : 1) : S <= 2 ? 4 : S <= 4 ? 2 : 1;
+}
 
 template <int V, int S>
 __device__ __forceinline__ void norm_fwd_block(const NormArgs& a, int b, float* affine) {
-  constexpr int R = RowsAtOnce<V, S>::value;
+  constexpr int R = rows_in_flight(V, S);
   const RowLanes<V, S> L(a, b);
   float *w = affine, *c = affine + L.len;
   expand_affine(a, b, w, c);
@@ -194,7 +201,7 @@ __device__ __forceinline__ void norm_fwd_block(const NormArgs& a, int b, float* 
 // MEAN: a 0e block.
 template <int V, int S, bool MEAN>
 __device__ __forceinline__ void norm_bwd_block(const NormArgs& a, int b, float* affine) {
-  constexpr int R = RowsAtOnce<V, S>::value;
+  constexpr int R = rows_in_flight(V, S);
   const RowLanes<V, S> L(a, b);
   expand_affine(a, b, affine, nullptr);
   const int per = kRowThreads / L.G, mine = threadIdx.x / L.G, cta = blockIdx.x - a.cta0[b], ctas = a.cta0[b + 1] - a.cta0[b];
@@ -306,7 +313,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(BWD, V * MOST)) k_nor
       else norm_bwd_block<V, n, false>(a, b, affine);                            \
     }                                                                            \
     break;
-  if constexpr (V == 4) {
+  if constexpr (V >= 2) {
     switch (a.S[b]) {
       TP_NORM_CASE(1)
       TP_NORM_CASE(2)
@@ -314,6 +321,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(BWD, V * MOST)) k_nor
       TP_NORM_CASE(4)
       TP_NORM_CASE(6)
       TP_NORM_CASE(9)
+      TP_NORM_CASE(18)
     }
   } else {
     switch (a.S[b]) {
@@ -557,25 +565,25 @@ tp_status_t parse_rows(const char* irreps, std::vector<IrrepTerm>& t, int& dim) 
   return TP_OK;
 }
 
-// Lanes and chunks a lane of each block: the fewest idle lanes among the forms with at most four chunks
-// (V = 4) or sixteen floats a lane, and of those with equally few the one with most lanes; a whole warp for
-// longer blocks.  Returns the most chunks a lane, 0 if a block is too long.
+// Lanes and chunks a lane of each block: the fewest idle lanes among the forms with at most sixteen floats a
+// lane, and of those with equally few the one with most lanes; a whole warp for longer blocks.  Returns the
+// most chunks a lane, 0 if a block is too long.
 int row_forms(NormArgs& a, int V) {
-  static const int slots4[] = {1, 2, 3, 4, 6, 9}, slots1[] = {1, 2, 4, 8, 16, 24, 36};
+  static const int slots4[] = {1, 2, 3, 4, 6, 9, 18}, slots1[] = {1, 2, 4, 8, 16, 24, 36};
   int most = 0;
   for (int b = 0; b < a.nb; ++b) {
     const int chunks = a.mul[b] * a.d[b] / V;
     a.S[b] = 0;
     for (int G = 32; G >= 1; G /= 2) {
       int S = 0;
-      if (V == 4) {
+      if (V >= 2) {
         for (int s : slots4)
-          if (S == 0 && s * G >= chunks) S = s;
+          if (S == 0 && s * G >= chunks && V * s <= 36) S = s;
       } else {
         for (int s : slots1)
           if (S == 0 && s * G >= chunks) S = s;
       }
-      if (S == 0 || (a.S[b] != 0 && (S > (V == 4 ? 4 : 16) || G * S >= a.G[b] * a.S[b]))) continue;
+      if (S == 0 || (a.S[b] != 0 && (S * V > 16 || G * S >= a.G[b] * a.S[b]))) continue;
       a.G[b] = G;
       a.S[b] = S;
     }
@@ -587,7 +595,7 @@ int row_forms(NormArgs& a, int V) {
 
 // Shares `total` CTAs out among the blocks by their floats, at least one each and none without a row.
 // `any`: one row a CTA and every CTA on all blocks (k_norm_any).
-void share_ctas(NormArgs& a, int64_t N, int total, bool any) {
+void share_ctas(NormArgs& a, int64_t N, int total, int V, bool any) {
   int64_t at = 0;
   a.cta0[0] = 0;
   for (int b = 0; b < a.nb; ++b) {
@@ -596,7 +604,7 @@ void share_ctas(NormArgs& a, int64_t N, int total, bool any) {
     if (any) {
       n = std::min<int64_t>(N, total);
     } else {
-      const int per = kRowThreads / a.G[b];
+      const int per = kRowThreads / a.G[b] * rows_in_flight(V, a.S[b]);
       n = std::min<int64_t>((N + per - 1) / per, ((int64_t)total * len + a.dim - 1) / a.dim);
     }
     n = std::max<int64_t>(n, 1);
@@ -609,6 +617,7 @@ void share_ctas(NormArgs& a, int64_t N, int total, bool any) {
 // CTAs of the backward pass: what is resident at once, each leaves a partial of the weight gradients.
 int most_slots(int most, int V) {
   if (V == 4) return most <= 1 ? 1 : most <= 2 ? 2 : most <= 4 ? 4 : most <= 6 ? 6 : 9;
+  if (V == 2) return most <= 2 ? 2 : most <= 4 ? 4 : most <= 9 ? 9 : 18;
   return most <= 4 ? 4 : most <= 8 ? 8 : most <= 16 ? 16 : 36;
 }
 int bwd_ctas(const NormArgs& a, int most, int V) {
@@ -616,14 +625,14 @@ int bwd_ctas(const NormArgs& a, int most, int V) {
   return 148 * ctas_per_sm(true, V * most_slots(most, V));
 }
 
-// Floats of the partials with either width of a chunk, so that the workspace does not depend on alignment.
-size_t part_floats(const NormArgs& proto, bool vec4, int64_t N) {
+// Floats of the partials with any width of a chunk up to `width`: the workspace does not depend on alignment.
+size_t part_floats(const NormArgs& proto, int width, int64_t N) {
   size_t n = 0;
-  for (int V : {1, 4}) {
-    if (V == 4 && !vec4) continue;
+  for (int V : {1, 2, 4}) {
+    if (V > width) continue;
     NormArgs a = proto;
     const int most = row_forms(a, V);
-    share_ctas(a, N, bwd_ctas(a, most, V), most == 0);
+    share_ctas(a, N, bwd_ctas(a, most, V), V, most == 0);
     const int b = a.nb - 1;
     n = std::max(n, (size_t)a.part_at[b] + (size_t)(a.cta0[b + 1] - a.cta0[b]) * 2 * a.mul[b] * a.d[b]);
   }
@@ -651,11 +660,22 @@ cudaError_t launch_norm(const NormArgs& a, int most, int V, cudaStream_t s) {
     case 4 * 8 + 4: return launch_most<BWD, 4, 4>(a, smem, s);
     case 6 * 8 + 4: return launch_most<BWD, 4, 6>(a, smem, s);
     case 9 * 8 + 4: return launch_most<BWD, 4, 9>(a, smem, s);
+    case 2 * 8 + 2: return launch_most<BWD, 2, 2>(a, smem, s);
+    case 4 * 8 + 2: return launch_most<BWD, 2, 4>(a, smem, s);
+    case 9 * 8 + 2: return launch_most<BWD, 2, 9>(a, smem, s);
+    case 18 * 8 + 2: return launch_most<BWD, 2, 18>(a, smem, s);
     case 4 * 8 + 1: return launch_most<BWD, 1, 4>(a, smem, s);
     case 8 * 8 + 1: return launch_most<BWD, 1, 8>(a, smem, s);
     case 16 * 8 + 1: return launch_most<BWD, 1, 16>(a, smem, s);
     default: return launch_most<BWD, 1, 36>(a, smem, s);
   }
+}
+
+// The widest chunk, up to `width` floats, that the pointers allow.
+int chunk_width(int width, const void* p, const void* q, const void* r) {
+  for (const void* t : {p, q, r})
+    while (reinterpret_cast<uintptr_t>(t) % (4 * width) != 0) width /= 2;
+  return width;
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -667,7 +687,7 @@ using namespace tp;
 
 struct tp_norm_s {
   NormArgs proto;
-  bool vec4;                 // every block's length is a multiple of four floats
+  int width;                 // the largest of 4, 2, 1 that divides every block's length
 };
 struct tp_dropout_s {
   DropoutArgs proto;
@@ -686,10 +706,10 @@ tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps) try 
   if (!((float)eps > 0.0f && (float)eps <= 3.0e38f)) return set_failure(TP_ERR_INVALID_ARG, "eps must be positive and finite");
   a.eps = (float)eps;
   int off = 0;
-  bool vec4 = true;
+  int width = 4;
   for (const IrrepTerm& b : t) {
     const int i = a.nb++;
-    vec4 = vec4 && b.mul * (2 * b.l + 1) % 4 == 0;
+    while (b.mul * (2 * b.l + 1) % width != 0) width /= 2;
     a.off[i] = off;
     a.mul[i] = b.mul;
     a.d[i] = 2 * b.l + 1;
@@ -705,7 +725,7 @@ tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps) try 
   }
   tp_norm_s* h = new tp_norm_s();
   h->proto = a;
-  h->vec4 = vec4;
+  h->width = width;
   *norm = h;
   return TP_OK;
 } catch (...) {
@@ -729,7 +749,7 @@ tp_status_t tp_norm_workspace_size(tp_norm_t norm, int64_t N, int32_t op, size_t
   if (!norm || !bytes) return set_failure(TP_ERR_INVALID_ARG, "NULL argument");
   if (N < 0) return set_failure(TP_ERR_INVALID_ARG, "N must be non-negative");
   if (op != TP_OP_FWD && op != TP_OP_BWD) return set_failure(TP_ERR_INVALID_ARG, "op must be TP_OP_FWD or TP_OP_BWD");
-  *bytes = op == TP_OP_FWD ? 0 : sizeof(float) * part_floats(norm->proto, norm->vec4, N);
+  *bytes = op == TP_OP_FWD ? 0 : sizeof(float) * part_floats(norm->proto, norm->width, N);
   return TP_OK;
 }
 
@@ -749,13 +769,13 @@ tp_status_t tp_norm_fwd(tp_norm_t norm, int64_t N, const float* x, const float* 
   a.bias = bias;
   a.y = y;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int V = norm->vec4 && al16(x) && al16(y) ? 4 : 1, most = row_forms(a, V);
+  const int V = chunk_width(norm->width, x, y, nullptr), most = row_forms(a, V);
   count_launches(1);
   if (most == 0) {
     k_norm_any<false><<<(unsigned)std::min<int64_t>(N, 148 * 16), kNormThreads, 0, s>>>(a);
     return cuda_status(cudaGetLastError(), "tp_norm_fwd");
   }
-  share_ctas(a, N, 148 * 8, false);
+  share_ctas(a, N, 148 * 8, V, false);
   return cuda_status(launch_norm<false>(a, most, V, s), "tp_norm_fwd");
 }
 
@@ -777,12 +797,12 @@ tp_status_t tp_norm_bwd(tp_norm_t norm, int64_t N, const float* x, const float* 
   a.gx = gx;
   a.gweight = gweight;
   a.gbias = gbias;
-  const size_t need = sums ? sizeof(float) * part_floats(a, norm->vec4, N) : 0;
+  const size_t need = sums ? sizeof(float) * part_floats(a, norm->width, N) : 0;
   if (sums && (!ws || ws_bytes < need)) return set_failure(TP_ERR_WORKSPACE, "workspace too small");
   a.part = sums ? static_cast<float*>(ws) : nullptr;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int V = norm->vec4 && al16(x) && al16(gy) && al16(gx) ? 4 : 1, most = row_forms(a, V);
-  share_ctas(a, N, bwd_ctas(a, most, V), most == 0);
+  const int V = chunk_width(norm->width, x, gy, gx), most = row_forms(a, V);
+  share_ctas(a, N, bwd_ctas(a, most, V), V, most == 0);
   cudaError_t e = cudaSuccess;
   count_launches(1);
   if (most == 0) {

@@ -144,6 +144,29 @@ def test_norm_in_place_parts_and_layouts(tp, irreps):
         assert_within(t, want[name], bound[name], name)
 
 
+@pytest.mark.parametrize("irreps,rows,start", [("2x0e", 1, 0), ("6x0e+2x1o", 45, 0), ("18x0o+18x1o+18x1e+18x2e", 391, 0), ("78x0o+78x1o+78x2e+78x3o", 130, 0),
+                                               ("1150x0e+6x0e", 40, 0), ("382x1o", 33, 0), ("30x0e+30x3o", 2003, 0), ("64x0e+32x1o", 130, 2),
+                                               ("1152x0e", 21, 2), ("8x0e", 1000, 2)])
+def test_norm_of_eight_byte_rows(tp, irreps, rows, start):
+    """Blocks of an even number of floats that is no multiple of four, and rows that start 8 bytes off."""
+    norm, rng = tp.Norm(irreps), np.random.default_rng(rows)
+    f = lambda *s: rng.standard_normal(s).astype(np.float32)
+    x, gy, w, b = f(rows, norm.dim) * 3 + 1, f(rows, norm.dim), f(norm.n_weights), f(norm.n_bias)
+
+    def laid(a):
+        buf = torch.full((rows * norm.dim + start,), 5.0, device="cuda")
+        buf[start:] = torch.as_tensor(a).cuda().flatten()
+        return buf[start:].view(rows, norm.dim)
+
+    y = tp.tp_norm_fwd(norm, laid(x), dev(w), dev(b), y=laid(gy))
+    gx, gw, gb = tp.tp_norm_bwd(norm, laid(x), laid(gy), dev(w), gx=laid(x))
+    want = oa.norm_backward(irreps, x, gy, w, b)
+    want["y"] = oa.norm(irreps, x, w, b)
+    bound = norm_bounds(irreps, x, w, b, gy, 1e-5)
+    for got, name in ((y, "y"), (gx, "gx"), (gw, "gweight"), (gb, "gbias")):
+        assert_within(got, want[name], bound[name], name)
+
+
 def test_norm_of_no_rows_and_repeats(tp):
     norm = tp.Norm("8x0e+8x1o")
     x = torch.zeros(0, norm.dim, device="cuda")
