@@ -22,7 +22,7 @@
 // windows of win = hub / 2 edges, whose CTAs come before those of the rows.  A window meets at
 // most two such rows (the row of its first edge and the row of its last one), finds them by a
 // 33-way search in the row pointers and leaves a partial row for each; a join kernel adds a row's
-// partials up in window order.  Graphs of at most `hub` edges have neither windows nor the join.
+// partials up in window order.  Graphs of at most 320 edges have neither windows nor the join.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -121,7 +121,7 @@ __host__ __device__ constexpr int ctas_per_sm(Pass pass, int V, int S) {
   return pass == kRecv ? 4 : 5;
 }
 
-constexpr int kMinWindow = 160;
+constexpr int kMinWindow = 64, kFewWindows = 160;
 
 // The kernels of one call follow each other by programmatic dependent launch: a kernel lets the next
 // one be set up from its start on, and the next one waits here, before it touches anything that an
@@ -955,18 +955,18 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
   }
 }
 
-// Joins the partial rows of the long rows, in window order: CTA w acts when such a row begins in window w.
-// Its eight warps take every eighth window, 128 floats of the row at a time, and are then added up in
-// order.  Forward: the windows' sums meet at their common maximum.  Bound by the reads of the partials,
+// Joins the partial rows of the long rows, in window order: CTA w acts when such a row begins in window w,
+// `cuts` CTAs a window share the row's floats, 128 at a time.  Its eight warps take every eighth window and
+// are then added up in order.  Forward: the windows' sums meet at their common maximum.  Bound by the reads of the partials,
 // one row for `win` edges' gathers of two.
 constexpr int kJoinThreads = 256;
 
 template <int PASS>   // 0: y, lse; 1: gq; 2: gk, gv
-__device__ __forceinline__ void join_long_row(const AttnArgs& a, int w, const float* parts, int part_len) {
+__device__ __forceinline__ void join_long_row(const AttnArgs& a, int cta, int cuts, const float* parts, int part_len) {
   __shared__ float top[32], total[32], sums[kJoinThreads / 32][128];
   const int32_t* ptr = PASS == 2 ? a.colptr : a.rowptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kJoinThreads / 32;
-  const int first = w * a.win, end = min(first + a.win, a.E);
+  const int cut = cta / a.n_win, w = cta - cut * a.n_win, first = w * a.win, end = min(first + a.win, a.E);
   int row, same;
   find_rows(ptr, a.N, end - 1, end - 1, row, same);   // the row pointers are the caller's: read before the wait
   wait_for_previous();
@@ -994,13 +994,13 @@ __device__ __forceinline__ void join_long_row(const AttnArgs& a, int w, const fl
         top[h] = ref;
         const bool none = m == -INFINITY && l == 0.0f;
         total[h] = none ? 0.0f : a.drop.inv_keep / l;
-        if (a.lse) a.lse[(int64_t)row * a.H + h] = none ? -INFINITY : m + logf(l);
+        if (a.lse && cut == 0) a.lse[(int64_t)row * a.H + h] = none ? -INFINITY : m + logf(l);
       }
     }
     __syncthreads();
   }
   const int width = PASS == 0 ? a.dv : PASS == 1 ? a.dq : a.dq + a.dv;
-  for (int d0 = 0; d0 < width; d0 += 128) {
+  for (int d0 = cut * 128; d0 < width; d0 += cuts * 128) {
     float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int head[4] = {0, 0, 0, 0};
     if (PASS == 0) {
@@ -1048,7 +1048,7 @@ __device__ __forceinline__ void join_long_row(const AttnArgs& a, int w, const fl
 }
 
 __global__ void __launch_bounds__(kJoinThreads) k_attn_fwd_join(const __grid_constant__ AttnArgs a) {
-  join_long_row<0>(a, blockIdx.x, a.part, a.part_len);
+  join_long_row<0>(a, blockIdx.x, gridDim.x / a.n_win, a.part, a.part_len);
 }
 
 // What is left of a backward pass: the long rows of gq (CTAs 0 .. recv_joins - 1) and of gk and gv (the
@@ -1061,9 +1061,9 @@ struct Tail {
 
 __global__ void __launch_bounds__(kJoinThreads) k_attn_bwd_tail(const __grid_constant__ AttnArgs a, const __grid_constant__ Tail t) {
   int cta = blockIdx.x;
-  if (cta < t.recv_joins) return join_long_row<1>(a, cta, t.recv_part, t.recv_len);
+  if (cta < t.recv_joins) return join_long_row<1>(a, cta, t.recv_joins / a.n_win, t.recv_part, t.recv_len);
   cta -= t.recv_joins;
-  if (cta < t.send_joins) return join_long_row<2>(a, cta, t.send_part, t.send_len);
+  if (cta < t.send_joins) return join_long_row<2>(a, cta, t.send_joins / a.n_win, t.send_part, t.send_len);
   cta -= t.send_joins;
   wait_for_previous();
   table_sum(a, cta * (kJoinThreads / 32) + (threadIdx.x >> 5));
@@ -1270,14 +1270,25 @@ cudaError_t launch_slots(Pass pass, AttnArgs& a, cudaStream_t s) {
   }
 }
 
-// Windows of at least 160 edges, and no more of them than 16 a SM: rows of up to twice that stay with their own
-// warps.  Fewer CTAs that look for long rows in vain against shorter ones for those there are: with 128 / 160 /
-// 192 / 256 edges 162,892 edges without a long row take 213 / 210 / 208 / 208 us backward, 311,027 edges with a
-// node of 8,192 neighbours 225 / 225 / 236 / 253.
+// Windows of 64 to 160 edges while there are four of them a SM, longer ones where there would be more than 16 a
+// SM; rows of up to twice that stay with their own warps.  Fewer CTAs that look for long rows in vain against
+// shorter ones for those there are.  With windows of 128 / 160 / 192 / 256 edges 162,892 edges without a long row
+// take 213 / 210 / 208 / 208 us backward, 311,027 edges with a node of 8,192 neighbours 225 / 225 / 236 / 253;
+// and with 160 edges against this rule 46,080 without a long row 16.5 against 17.0 us forward, 42,112 edges with
+// a node of 2,942 neighbours 68 against 45, 10,834 edges in rows of up to 255 of 1,534 floats 129 against 72.
+// Graphs of up to 320 edges do without the join's launch (192 edges: 4.7 us, 5.5 with it).
 void window_plan(AttnArgs& a) {
-  a.win = std::max(kMinWindow, (a.E / (148 * 16) + 32) / 32 * 32);
+  const auto each = [&](int per_sm) { return (a.E / (148 * per_sm) + 32) / 32 * 32; };
+  a.win = std::max({kMinWindow, std::min(kFewWindows, each(4)), each(16)});
   a.hub = 2 * a.win;
-  a.n_win = a.E > a.hub ? (a.E + a.win - 1) / a.win : 0;
+  a.n_win = a.E > 2 * kFewWindows ? (a.E + a.win - 1) / a.win : 0;
+}
+
+// CTAs of the join of rows of `width` floats: as many a window as have 128 floats of the row each, while that
+// keeps them to four a SM.  13,765 edges with a node of 1,617 neighbours, 672 floats a row: 75 us forward with one
+// CTA a window, 68 so; with 16 a SM 66, but 46,080 edges without a long row 37.3 instead of 35.6 backward.
+int join_ctas(const AttnArgs& a, int width) {
+  return a.n_win * (a.n_win == 0 ? 0 : std::max(1, std::min((width + 127) / 128, 148 * 4 / a.n_win)));
 }
 
 int part_len(const AttnArgs& a, Pass pass) {
@@ -1506,7 +1517,7 @@ tp_status_t tp_attn_fwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int width = chunk_width(attn->width, {q, k, v, y}, {ldq, ldk, ldv});
   cudaError_t e = launch_pass(kFwd, a, width, static_cast<float*>(ws), s);
-  if (e == cudaSuccess && a.n_win > 0) e = launch_after(k_attn_fwd_join, (unsigned)a.n_win, kJoinThreads, 0, s, a);
+  if (e == cudaSuccess && a.n_win > 0) e = launch_after(k_attn_fwd_join, (unsigned)join_ctas(a, a.dv), kJoinThreads, 0, s, a);
   return cuda_status(e, "tp_attn_fwd");
 }
 
@@ -1578,8 +1589,8 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   tail.send_part = reinterpret_cast<float*>(w + L.send_part);
   tail.recv_len = part_len(a, kRecv);
   tail.send_len = part_len(a, kSend);
-  tail.recv_joins = gq ? a.n_win : 0;
-  tail.send_joins = send ? a.n_win : 0;
+  tail.recv_joins = gq ? join_ctas(a, a.dq) : 0;
+  tail.send_joins = send ? join_ctas(a, a.dq + a.dv) : 0;
   // behind the sender pass while a copy of the table leaves that pass's CTAs their shared memory
   a.table_here = gtable && E > 0 && send && (size_t)a.K * a.H * sizeof(float) <= 32 * 1024;
   a.hist_ctas = 0;

@@ -141,6 +141,24 @@ def test_one_receiver_and_its_edges(tp, edges):
     check(pr, solve(tp, pr))
 
 
+@pytest.mark.parametrize("qk,v,heads", [("64x0e+32x1o+32x2e", "64x0e+32x1o+32x3o", 8), ("301x0e", "301x3o", 1), ("2x0e+2x1o", "130x0e", 2), ("1x0e", "129x0e", 1)])
+def test_long_rows_of_many_floats(tp, qk, v, heads):
+    """Rows of 63 to 193 edges, around the shortest window and twice it, whose joins are cut by the floats of the
+    row; one of them in windows that are masked as a whole."""
+    counts = np.array([3, 127, 128, 0, 129, 130, 63, 64, 65, 193, 1, 160, 2, 191])
+    n, rng = len(counts), np.random.default_rng(8)
+    rowptr = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    src = rng.integers(0, n, rowptr[-1]).astype(np.int32)
+    src[rng.random(len(src)) < 0.3] = 7                        # a sender of some 400 edges
+    pr = problem(9, qk, v, heads, n, 0, p=0.2, graph=(rowptr, src))
+    d = pr["d"]
+    d["bucket"][rowptr[9]:rowptr[9] + 140] = -1
+    d["bucket"][rowptr[5]:rowptr[6]] = -1                      # and a long row that hears nobody
+    got = solve(tp, pr)
+    assert bool((got["lse"][5] == -math.inf).all()) and bool((got["y"][5] == 0).all()) and bool((got["gq"][5] == 0).all())
+    check(pr, got)
+
+
 def test_masks_that_leave_a_row_nothing(tp):
     pr = problem(7, "8x0e+4x1o", "8x0e+4x1o", 4, n=30, mean_degree=6, spare=5)
     d = pr["d"]
