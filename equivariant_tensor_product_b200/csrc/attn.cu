@@ -591,6 +591,46 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
   }
 }
 
+// A row whose log-sum lies far from zero (a constant bias, a mask of the lowest float on every edge) has lost in
+// the rounding of lse = m + log l what normalises it: half a unit in the last place is 6e-5 at 2^10, the whole of
+// log l from 2^24 on, and exp(s - lse) would be off by as much.  Such rows get the maximum and the sum of their
+// exponentials again, from one more sweep over the whole row's rows of k by every task of the row: rare enough
+// for a sweep that every window of a long row repeats.  Rows that are not far pay one subtraction an edge
+// (whole step: 46,080 edges 53.0 -> 53.2 us, 165,448 edges of 320 floats 725 -> 733).
+constexpr float kFarLse = 1024.0f;
+__device__ __forceinline__ bool far_from_zero(float lse) { return fabsf(lse) >= kFarLse && fabsf(lse) < INFINITY; }
+
+template <int V, int SQ, int N, bool WIDE>
+__device__ __forceinline__ void row_statistics(const AttnArgs& a, const Lane<V, WIDE>& L, int row, const Vec<V> (&q)[SQ],
+                                               const uint32_t (&oq)[SQ], float* join, int& turn, float& top, float& l) {
+  const int lo = clamp_edge(__ldg(a.rowptr + row), a.E), hi = clamp_edge(__ldg(a.rowptr + row + 1), a.E);
+  for (int e0 = lo; e0 < hi; e0 += N) {
+    float dot[N], bias[N];                 // bias -inf: takes no part
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int e = min(e0 + u, hi - 1), j = __ldg(a.src + e), b = a.bucket ? __ldg(a.bucket + e) : 0;
+      const bool on = e0 + u < hi && (unsigned)j < (unsigned)a.N && (!a.bucket || (unsigned)b < (unsigned)a.K);
+      bias[u] = !on ? -INFINITY : a.table && L.live ? __ldg(a.table + (int64_t)b * a.H + L.h) : 0.0f;
+      dot[u] = 0.0f;
+      const char* k_row = row_at(a.k, on ? j : 0, a.ldk);
+#pragma unroll
+      for (int s = 0; s < SQ; ++s) {
+        const Vec<V> x = load_vec<V, true>(k_row + oq[s], on && L.has(a.mq, s));
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot[u] = fmaf(q[s].x[i], x.x[i], dot[u]);
+      }
+    }
+    L.sum(dot, join, turn);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (bias[u] == -INFINITY) continue;
+      const float s = fmaf(dot[u], a.scale, bias[u]), high = fmaxf(top, s);
+      l = l * exp_of(top - high) + exp_of(s - high);
+      top = high;
+    }
+  }
+}
+
 // Backward, receiver order: gq, and for the sender pass and gtable (ds, r p) of every live edge and head
 // and the receiver of every edge.
 template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
@@ -631,8 +671,19 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
       for (int i = 0; i < V; ++i) delta[0] = fmaf(gy[s].x[i], y.x[i], delta[0]);
     }
     L.sum(delta, join, turn);
-    const float del = delta[0];
-    const float lse = L.live ? __ldg(a.lse_in + (int64_t)t.row * a.H + L.h) : 0.0f;
+    float del = delta[0];
+    // p = w exp((s - less) - shift): less = lse, or shift = the maximum and w = 1 / the sum where the row is far
+    float less = L.live ? __ldg(a.lse_in + (int64_t)t.row * a.H + L.h) : 0.0f, shift = 0.0f, kept = a.drop.inv_keep;
+    if (__any_sync(kFull, far_from_zero(less))) {
+      float top = -INFINITY, l = 0.0f;
+      row_statistics<V, SQ, WIDE ? 2 * U : 2, WIDE>(a, L, t.row, q, oq, join, turn, top, l);
+      if (far_from_zero(less) && l > 0.0f) {
+        less = 0.0f;
+        shift = top;
+        kept /= l;
+        del /= l;
+      }
+    }
     for (int base = t.lo; base < t.hi; base += 32) {
       const EdgeLane mine = read_edge(a, key, base + lane, base + lane < t.hi, t.head0, a.hw);
       if (a.rec && base + lane < t.hi && t.head0 == 0 && (!WIDE || threadIdx.x < 32))
@@ -660,9 +711,9 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
         for (int k = 0; k < 4; ++k) {
           const int i = i0 + k * L.step();
           if (i >= n) break;
-          const bool out = bias[k] == -INFINITY || lse == -INFINITY;
+          const bool out = bias[k] == -INFINITY || less == -INFINITY;
           any_out |= out;
-          w2[i * a.hw + L.sub] = make_float2(out ? -INFINITY : bias[k] - lse, (B.c[i] >> L.sub) & 1u ? a.drop.inv_keep : 0.0f);
+          w2[i * a.hw + L.sub] = make_float2(out ? -INFINITY : bias[k] - less, (B.c[i] >> L.sub) & 1u ? kept : 0.0f);
         }
       }
       any_out = __any_sync(kFull, any_out);
@@ -702,7 +753,7 @@ __global__ void __launch_bounds__(WIDE ? kAttnWideThreads : kAttnThreads, WIDE ?
           if (t0 + u >= n) break;
           float2& w = w2[(t0 + u) * a.hw + L.sub];
           const bool out = any_out && w.x == -INFINITY;
-          const float p = out ? 0.0f : exp_of(fmaf(dot[u], a.scale, w.x));
+          const float p = out ? 0.0f : exp_of(fmaf(dot[u], a.scale, w.x) - shift);
           const float pr = p * w.y, ds = out ? 0.0f : fmaf(pr, dot[U + u], -p * del);
           __syncwarp();
           if (L.first() == 0) w = make_float2(ds, out ? -0.0f : pr);

@@ -19,6 +19,10 @@
  *   gq[i] = scale sum_e ds k[j]      gk[j] = scale sum_{e from j} ds q[i]
  *   gv[j] = sum_{e from j} r p gy[i] gtable[b,h] = sum_{e: bucket[e] = b} ds[e,h]
  *
+ * Where |lse| >= 2^10 (a large constant in the table, a mask of the lowest float on every edge of a
+ * row), lse in 32 bits no longer holds the row's sum; the probabilities are then formed again from q
+ * and k alone, one more sweep over those rows' edges.
+ *
  * First order only.  The bias is constant within a bucket: no gradient reaches the edge vectors.
  *
  * What takes no part.  An edge whose bucket lies outside [0, n_buckets) (tp_distance_buckets
