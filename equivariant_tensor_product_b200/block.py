@@ -191,9 +191,10 @@ def tp_norm_bwd(norm: Norm, x, gy, weight=None, need_gx=True, need_gweight=True,
         gx = torch.empty(shape, dtype=torch.float32, device=dev) if gx is None and need_gx else gx
         gweight = torch.empty(norm.n_weights, dtype=torch.float32, device=dev) if gweight is None and need_gweight else gweight
         gbias = torch.empty(norm.n_bias, dtype=torch.float32, device=dev) if gbias is None and need_gbias else gbias
-        if norm._size is None or norm._size[0] != N:
-            norm._size = (N, tp_norm_workspace_size(norm, N, TP_OP_BWD))
-        ws, ws_ptr, ws_bytes = workspace(ws, norm._size[1], i)
+        size = norm._size             # looked at once: another thread's call may replace it
+        if size is None or size[0] != N:
+            size = norm._size = (N, tp_norm_workspace_size(norm, N, TP_OP_BWD))
+        ws, ws_ptr, ws_bytes = workspace(ws, size[1], i)
         check(norm._lib.tp_norm_bwd(norm.handle, N, f32(x, i, shape, "x"), f32(weight, i, (norm.n_weights,), "weight"),
                                     f32(gy, i, shape, "gy"), f32(gx, i, shape, "gx"),
                                     f32(gweight, i, (norm.n_weights,), "gweight"), f32(gbias, i, (norm.n_bias,), "gbias"),

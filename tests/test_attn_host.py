@@ -198,3 +198,35 @@ def test_no_cpu_path_without_a_device(tp):
     assert lib.tp_norm_fwd(tp.Norm("4x0e").handle, 4, FAKE, FAKE, FAKE, FAKE, None) == 5
     assert lib.tp_dropout_fwd(tp.Dropout("4x0e").handle, 4, FAKE, 0.5, FAKE, 0, FAKE, None) == 5
     assert lib.tp_distance_buckets(4, FAKE, 3, FAKE, 5.0, FAKE, None) == 5
+
+
+def test_norm_on_one_handle_from_two_threads(tp, monkeypatch):
+    """Between a backward call's look at the handle's workspace size and its use, another thread's call with
+    other rows may change it."""
+    from equivariant_tensor_product_b200 import block
+    asked = []
+
+    class Handle:
+        dim, n_weights, n_bias, handle = 4, 4, 4, None
+        looks = 0
+
+        class _lib:
+            tp_norm_bwd = staticmethod(lambda *a: 0)
+
+        @property
+        def _size(self):
+            self.looks += 1
+            return (3, 48) if self.looks == 1 else (1000, 16000)
+
+        @_size.setter
+        def _size(self, value):
+            pass
+    monkeypatch.setattr(block, "device_index", lambda t, name: 0)
+    monkeypatch.setattr(block, "on", lambda i, stream: torch.no_grad())
+    monkeypatch.setattr(block, "f32", lambda *a: None)
+    monkeypatch.setattr(block, "stream_of", lambda i: 0)
+    monkeypatch.setattr(block, "workspace", lambda ws, need, i: asked.append(need) or (None, None, need))
+    monkeypatch.setattr(block, "tp_norm_workspace_size", lambda norm, N, op: 16 * N)
+    x = torch.zeros(3, 4)
+    tp.tp_norm_bwd(Handle(), x, x)
+    assert asked == [48]
