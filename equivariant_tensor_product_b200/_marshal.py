@@ -9,7 +9,6 @@ import torch
 
 _F32 = torch.float32
 _NO_CONTEXT = contextlib.nullcontext()
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def device_index(t, name):
@@ -34,7 +33,7 @@ def on(index, stream):
 
 
 def stream_of(index):
-    return _raw_stream(index)
+    return torch._C._cuda_getCurrentRawStream(index)     # looked up here: a torch without CUDA has none
 
 
 def _refuse(t, dtype, index, shape, name):

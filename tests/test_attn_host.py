@@ -3,6 +3,9 @@
 the device, and no CPU path."""
 import ctypes as C
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -230,3 +233,11 @@ def test_norm_on_one_handle_from_two_threads(tp, monkeypatch):
     x = torch.zeros(3, 4)
     tp.tp_norm_bwd(Handle(), x, x)
     assert asked == [48]
+
+
+def test_import_needs_no_cuda_build_of_torch(tp):
+    """Plans, their sizes and refusals are host code: a torch without CUDA lacks the raw-stream function."""
+    code = ("import torch; del torch._C._cuda_getCurrentRawStream; import equivariant_tensor_product_b200 as tp; "
+            "print(tp.Norm('4x0e+4x1o').dim)")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
+    assert r.returncode == 0 and r.stdout.split() == ["16"], r.stderr[-2000:]
