@@ -703,7 +703,8 @@ tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps) try 
   std::memset(&a, 0, sizeof(a));
   tp_status_t st = parse_rows(irreps, t, a.dim);
   if (st != TP_OK) return st;
-  if (!((float)eps > 0.0f && (float)eps <= 3.0e38f)) return set_failure(TP_ERR_INVALID_ARG, "eps must be positive and finite");
+  // squares below 2^-126 are flushed to zero, at most 2^-26 of such an eps
+  if (!((float)eps >= 1.0e-30f && (float)eps <= 3.0e38f)) return set_failure(TP_ERR_INVALID_ARG, "eps must be at least 1e-30 and finite");
   a.eps = (float)eps;
   int off = 0;
   int width = 4;

@@ -130,7 +130,7 @@ typedef struct tp_norm_s* tp_norm_t;
 typedef struct tp_dropout_s* tp_dropout_t;
 
 /* Builds a norm of rows of `irreps` (l <= 3, at most 16 blocks, rows of at most 8,192 floats);
- * eps > 0 and finite. */
+ * eps at least 1e-30 and finite (squares and sums are formed in 32 bits: floats beyond 1e18 overflow there). */
 tp_status_t tp_norm_create(tp_norm_t* norm, const char* irreps, double eps);
 tp_status_t tp_norm_destroy(tp_norm_t norm);
 /* Row width, entries of weight (channels) and of bias (0e channels). */

@@ -241,3 +241,13 @@ def test_import_needs_no_cuda_build_of_torch(tp):
             "print(tp.Norm('4x0e+4x1o').dim)")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=os.path.dirname(os.path.dirname(__file__)))
     assert r.returncode == 0 and r.stdout.split() == ["16"], r.stderr[-2000:]
+
+
+def test_norm_refuses_an_eps_that_squares_in_32_bits_cannot_stand_beside(tp):
+    """Squares below 2^-126 are flushed to zero: beside an eps near it they would be missing from the mean square,
+    and an eps below it is zero itself, which makes a NaN of a zero row."""
+    for eps in (1e-45, 1e-40, 1e-38, 9e-31):
+        with pytest.raises(tp.TPError) as e:
+            tp.Norm("4x0e+4x1o", eps)
+        assert e.value.status == 1
+    tp.Norm("4x0e+4x1o", 1.1e-30)

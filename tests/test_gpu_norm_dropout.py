@@ -400,3 +400,18 @@ def test_no_device_memory_with_buffers_given(tp):
     step()
     torch.cuda.synchronize()
     assert torch.cuda.max_memory_allocated() == before and torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.parametrize("irreps", ["16x0e+8x1o", "7x0e+5x1o", "1201x0e"])
+def test_norm_with_the_smallest_eps(tp, irreps):
+    """Zero rows stay zero and rows of squares below the smallest normal float are as good as their eps allows."""
+    norm, rng = tp.Norm(irreps, 1.1e-30), np.random.default_rng(0)
+    x = rng.standard_normal((6, norm.dim)).astype(np.float32)
+    x[0], x[1:] = 0, x[1:] * np.array([1e-15, 1e-17, 1e-19, 1e-20, 1.0], np.float32)[:, None]
+    y = tp.tp_norm_fwd(norm, dev(x))
+    assert bool((y[0] == 0).all())
+    eps = float(np.float32(1.1e-30))
+    bound = norm_bounds(irreps, x, None, None, x, eps)["y"]
+    want = oa.norm(irreps, x, eps=eps)
+    # every flushed square takes at most 2^-126 from the mean square, 2^-27 of eps
+    assert_within(y, want, bound + 2.0 ** -27 * np.abs(want.numpy()), "y")
