@@ -77,6 +77,13 @@ def rows(t, index, n, width, name):
     return t.data_ptr() or None, ld
 
 
+def apart(outputs, inputs, names):
+    """Refuses an output that starts where an input or another output does (one tensor given twice); None: not there."""
+    given = [p for p in outputs if p]
+    if len(set(given)) != len(given) or not set(given).isdisjoint(inputs):
+        raise ValueError(f"{names} must not share memory with an input or with one another")
+
+
 def workspace(ws, need, index):
     """(tensor that keeps it, pointer, bytes)"""
     if ws is None:

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from ._lib import TP_OP_BWD, TP_OP_FWD, check, load
-from ._marshal import device_index, f32, on, ptr, rows, stream_of, workspace
+from ._marshal import apart, device_index, f32, on, ptr, rows, stream_of, workspace
 
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
@@ -81,12 +81,19 @@ def _inputs(attn, rowptr, src, q, k, v, bucket, table, scale, p, rng, site):
         ptr(rng, _I64, i, (2,), "rng"), int(site))
 
 
+def _pointers(args):
+    """bucket, q, k, v, table and rng of what _inputs returns."""
+    return args[0], args[1], args[3], args[5], args[7], args[10]
+
+
 def tp_attn_fwd(attn: Attention, rowptr, src, q, k, v, bucket=None, table=None, scale: Optional[float] = None,
                 p: float = 0.0, rng=None, site: int = 0, y=None, lse=None, need_lse: bool = True, ws=None,
                 stream=None):
     """(y [N, v_dim], lse [N, heads]); lse is None when need_lse is False.  scale: default
-    1/sqrt(floats of a head of q).  p > 0 drops probabilities with rng = int64 CUDA tensor (seed, offset)."""
+    1/sqrt(floats of a head of q).  p > 0 drops probabilities with rng = int64 CUDA tensor (seed, offset).  y, lse
+    and ws may not share memory with an input."""
     N, E, i, graph, args = _inputs(attn, rowptr, src, q, k, v, bucket, table, scale, p, rng, site)
+    given = y is not None or lse is not None or ws is not None
     with on(i, stream):
         dev = q.device
         if y is None:
@@ -94,8 +101,10 @@ def tp_attn_fwd(attn: Attention, rowptr, src, q, k, v, bucket=None, table=None, 
         if lse is None and need_lse:
             lse = torch.empty(N, attn.heads, dtype=_F32, device=dev)
         ws, ws_ptr, ws_bytes = workspace(ws, _workspace_size(attn, N, E, TP_OP_FWD), i)
-        check(attn._lib.tp_attn_fwd(attn.handle, N, E, *graph, *args, f32(y, i, (N, attn.v_dim), "y"),
-                                    f32(lse, i, (N, attn.heads), "lse"), ws_ptr, ws_bytes, stream_of(i)), "tp_attn_fwd")
+        out = f32(y, i, (N, attn.v_dim), "y"), f32(lse, i, (N, attn.heads), "lse")
+        if given:
+            apart((*out, ws_ptr), (*graph, *_pointers(args)), "y, lse and the workspace")
+        check(attn._lib.tp_attn_fwd(attn.handle, N, E, *graph, *args, *out, ws_ptr, ws_bytes, stream_of(i)), "tp_attn_fwd")
     return y, lse
 
 
@@ -104,7 +113,8 @@ def tp_attn_bwd(attn: Attention, rowptr, src, q, k, v, y, lse, gy, bucket=None, 
                 need_gq=True, need_gk=True, need_gv=True, need_gtable: Optional[bool] = None, gq=None, gk=None,
                 gv=None, gtable=None, ws=None, stream=None):
     """(gq, gk, gv, gtable) against gy, each None when not requested; y and lse from tp_attn_fwd with the same
-    arguments.  need_gtable: default whenever there is a table.  gq, gk, gv may be column slices."""
+    arguments.  need_gtable: default whenever there is a table.  gq, gk, gv may be column slices, but share no
+    memory with an input or one another."""
     if (colptr is None) != (perm is None):
         raise ValueError("colptr and perm must both be given or both be None")
     N, E, i, graph, args = _inputs(attn, rowptr, src, q, k, v, bucket, table, scale, p, rng, site)
@@ -112,6 +122,7 @@ def tp_attn_bwd(attn: Attention, rowptr, src, q, k, v, y, lse, gy, bucket=None, 
         need_gtable = table is not None or gtable is not None
     qk, vd = attn.qk_dim, attn.v_dim
     table_shape = (attn.n_buckets, attn.heads)
+    given = any(t is not None for t in (gq, gk, gv, gtable, ws))
     with on(i, stream):
         dev = q.device
         gq = torch.empty(N, qk, dtype=_F32, device=dev) if gq is None and need_gq else gq
@@ -119,11 +130,14 @@ def tp_attn_bwd(attn: Attention, rowptr, src, q, k, v, y, lse, gy, bucket=None, 
         gv = torch.empty(N, vd, dtype=_F32, device=dev) if gv is None and need_gv else gv
         gtable = torch.empty(table_shape, dtype=_F32, device=dev) if gtable is None and need_gtable else gtable
         ws, ws_ptr, ws_bytes = workspace(ws, _workspace_size(attn, N, E, TP_OP_BWD), i)
-        check(attn._lib.tp_attn_bwd(attn.handle, N, E, *graph, ptr(colptr, _I32, i, (N + 1,), "colptr"),
-                                    ptr(perm, _I32, i, (E,), "perm"), *args, f32(y, i, (N, vd), "y"),
-                                    f32(lse, i, (N, attn.heads), "lse"), f32(gy, i, (N, vd), "gy"),
-                                    *rows(gq, i, N, qk, "gq"), *rows(gk, i, N, qk, "gk"), *rows(gv, i, N, vd, "gv"),
-                                    f32(gtable, i, table_shape, "gtable"), ws_ptr, ws_bytes, stream_of(i)), "tp_attn_bwd")
+        order = ptr(colptr, _I32, i, (N + 1,), "colptr"), ptr(perm, _I32, i, (E,), "perm")
+        saved = f32(y, i, (N, vd), "y"), f32(lse, i, (N, attn.heads), "lse"), f32(gy, i, (N, vd), "gy")
+        out = (*rows(gq, i, N, qk, "gq"), *rows(gk, i, N, qk, "gk"), *rows(gv, i, N, vd, "gv"),
+               f32(gtable, i, table_shape, "gtable"))
+        if given:
+            apart((*out[::2], ws_ptr), (*graph, *order, *_pointers(args), *saved), "gq, gk, gv, gtable and the workspace")
+        check(attn._lib.tp_attn_bwd(attn.handle, N, E, *graph, *order, *args, *saved, *out, ws_ptr, ws_bytes, stream_of(i)),
+              "tp_attn_bwd")
     return gq, gk, gv, gtable
 
 

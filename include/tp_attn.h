@@ -20,8 +20,8 @@
  *   gv[j] = sum_{e from j} r p gy[i] gtable[b,h] = sum_{e: bucket[e] = b} ds[e,h]
  *
  * Where |lse| >= 2^10 (a large constant in the table, a mask of the lowest float on every edge of a
- * row), lse in 32 bits no longer holds the row's sum; the probabilities are then formed again from q
- * and k alone, one more sweep over those rows' edges.
+ * row), lse in 32 bits no longer holds the row's sum; the backward pass then forms it again from q, k
+ * and table, in one more sweep over those rows' edges.
  *
  * First order only.  The bias is constant within a bucket: no gradient reaches the edge vectors.
  *
@@ -43,7 +43,9 @@
  * Layouts: fp32, q/k/v and gq/gk/gv rows ld* floats apart (ld >= the row's width: the three
  * may be slices of one [N, 2 qk_dim + v_dim] array); y, gy [N, v_dim], lse [N, H], table
  * [n_buckets, H], bucket [E] int32.  Outputs are fully overwritten, rows without edges with
- * zeros.  Results do not depend on the schedule: no floating-point atomics, fixed orders.
+ * zeros.  No output (the workspace is one) may share memory with an input or another output: rows
+ * of q, k, v and gy are read until the call ends, by other rows' sums too.  Results do not depend on
+ * the schedule: no floating-point atomics, fixed orders.
  *
  * Ownership, streams and errors as in tp.h; the library owns only the handle (host memory).
  * Calls on one handle from several threads or streams are independent as long as their

@@ -251,3 +251,22 @@ def test_norm_refuses_an_eps_that_squares_in_32_bits_cannot_stand_beside(tp):
             tp.Norm("4x0e+4x1o", eps)
         assert e.value.status == 1
     tp.Norm("4x0e+4x1o", 1.1e-30)
+
+
+def test_outputs_may_not_start_where_inputs_do(tp):
+    from equivariant_tensor_product_b200._marshal import apart
+    apart((16, None, 64), (None, 32, 48), "outputs")
+    apart((None, None), (None, 32), "outputs")
+    for outputs, inputs in (((16, 32), (32, 48)), ((16, 16), (32, 48)), ((None, 48), (None, 48))):
+        with pytest.raises(ValueError, match="share memory"):
+            apart(outputs, inputs, "outputs")
+
+
+def test_rows_are_refused_for_their_strides(tp):
+    """The device index of CPU tensors is -1: with it the check of the strides is reached."""
+    from equivariant_tensor_product_b200._marshal import rows
+    for bad in (torch.zeros(4, 16).t(), torch.zeros(1, 4).expand(16, 4), torch.zeros(16, 8)[:, ::2]):
+        with pytest.raises(ValueError, match="contiguous rows"):
+            rows(bad, -1, 16, 4, "q")
+    wide = torch.zeros(16, 8)
+    assert rows(wide[:, 4:], -1, 16, 4, "q") == (wide.data_ptr() + 16, 8)

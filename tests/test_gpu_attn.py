@@ -475,3 +475,20 @@ def test_buckets_of_an_unaligned_slice(tp):
     out = torch.full((502,), 77, dtype=torch.int32, device="cuda")
     tp.tp_distance_buckets(flat[:1500].view(500, 3), bounds, 2.5, bucket=out[1:501])
     assert int(out[0]) == 77 and int(out[501]) == 77
+
+
+def test_outputs_in_place_of_inputs_are_refused(tp):
+    """Other rows' sums still read q, k, v and gy while a row's outputs are written."""
+    pr = problem(40, "8x0e", "8x0e", 2, n=20, mean_degree=5)
+    g = {k: dev(a) for k, a in pr["d"].items()}
+    attn = tp.Attention("8x0e", "8x0e", 2, 5)
+    rows, more = (g["rowptr"], g["src"], g["q"], g["k"], g["v"]), dict(bucket=g["bucket"], table=g["table"])
+    for name in ("q", "k", "v"):
+        with pytest.raises(ValueError, match="share memory"):
+            tp.tp_attn_fwd(attn, *rows, y=g[name], **more)
+    y, lse = tp.tp_attn_fwd(attn, *rows, y=torch.empty(20, 8, device="cuda"), **more)
+    own = torch.empty(20, 8, device="cuda")
+    for given in (dict(gq=g["q"]), dict(gk=g["k"]), dict(gv=g["gy"]), dict(gv=y), dict(gtable=g["table"]), dict(gq=own, gk=own)):
+        with pytest.raises(ValueError, match="share memory"):
+            tp.tp_attn_bwd(attn, *rows, y, lse, g["gy"], **given, **more)
+    tp.tp_attn_bwd(attn, *rows, y, lse, g["gy"], gq=own, **more)
