@@ -415,3 +415,50 @@ def test_norm_with_the_smallest_eps(tp, irreps):
     want = oa.norm(irreps, x, eps=eps)
     # every flushed square takes at most 2^-126 from the mean square, 2^-27 of eps
     assert_within(y, want, bound + 2.0 ** -27 * np.abs(want.numpy()), "y")
+
+
+@pytest.mark.parametrize("irreps,rows", [("1x0e", 4736), ("1x0e", 4737), ("3x1o", 30011), ("1x0e", 120001), ("2x0e", 500009), ("7x0e+5x1o", 30011),
+                                         ("4x0e+4x1o", 120001), ("5x0o", 7105), ("32x0e+32x1o", 14209), ("31x0e+31x1o", 4737),
+                                         ("128x0e", 30011), ("32x0e+32x1o+32x2e", 9473), ("33x0e+33x1o", 20001), ("129x0e", 9471)])
+def test_dropout_of_many_rows(tp, irreps, rows):
+    """Several narrow rows a warp, tiles that end short, and more rows than warps."""
+    import attn_fast
+    drop, rng = tp.Dropout(irreps), np.random.default_rng(rows)
+    x = rng.standard_normal((rows, drop.dim)).astype(np.float32)
+    seed, offset, site, p = 11, 1 << 35, 2, 0.3
+    r = torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
+    y = tp.tp_dropout_fwd(drop, dev(x), p, r, site)
+    keep = attn_fast.keep_values(seed, offset + site, rows * drop.n_channels, p).reshape(rows, -1)
+    ir = Irreps(irreps)
+    want = x.astype(np.float64) * np.concatenate([np.repeat(keep[:, c:c + mul], 2 * l + 1, 1)
+                                                  for (mul, l, _), c in zip(ir.blocks, np.cumsum([0] + [m for m, _, _ in ir.blocks]))], 1)
+    # one rounding of 1/(1-p) and one of the product
+    assert_within(y, torch.as_tensor(want), 2 * U * np.abs(want) * (1 + 2 * U), "y")
+    assert torch.equal(y == 0, dev(want) == 0)
+    own = dev(x)
+    assert tp.tp_dropout_fwd(drop, own, p, r, site, y=own) is own and torch.equal(own, y)
+    buf = torch.full((rows * drop.dim + 2,), 5.0, device="cuda")
+    tp.tp_dropout_fwd(drop, dev(x), p, r, site, y=buf[1:-1].view(rows, drop.dim))
+    assert torch.equal(buf[1:-1].view(rows, drop.dim), y) and float(buf[0]) == 5.0 and float(buf[-1]) == 5.0
+
+
+def test_layer_gradient_against_differences_of_its_own_forward(tp):
+    P, rowptr, src, vec, x, gy = _make_layer(tp, seed=1)
+    x.requires_grad_(True)
+    graph, rng = tp.autograd.Graph(dev(rowptr), dev(src)), torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+    y = _layer(tp, P, x, graph, dev(vec), rng, 0.2)
+    (gx,) = torch.autograd.grad(y, x, gy)
+    step, eps = torch.randn(x.shape, generator=torch.Generator().manual_seed(1)).cuda(), 2.0 ** -5
+    dot = lambda a, b: float((a.double() * b.double()).sum())
+    with torch.no_grad():
+        ends = [x + s * eps * step for s in (1, -1)]
+        own = dot(_layer(tp, P, ends[0], graph, dev(vec), rng, 0.2).double() - _layer(tp, P, ends[1], graph, dev(vec), rng, 0.2).double(), gy)
+        exact = [_oracle_layer(P, a, rowptr, src, vec, 0.2, 3, 4)[0].detach() for a in ends]
+    want_y, want_x, _ = _oracle_layer(P, x, rowptr, src, vec, 0.2, 3, 4)
+    (want,) = torch.autograd.grad(want_y, want_x, gy.double().cpu())
+    # the quotient is off by its truncation, which the same quotient in 64 bits tells, and by the roundings of two
+    # forward passes: sums of at most 24 terms in four operators, 64 u of the largest output each
+    truncation = abs(dot(exact[0] - exact[1], gy.cpu()) / (2 * eps) - dot(want, step.cpu()))
+    rounding = 2 * float(gy.abs().sum()) * 64 * U * float(y.detach().abs().max()) / (2 * eps)
+    assert truncation + rounding <= 0.1 * float(gx.norm())     # the size of a derivative along a random direction
+    assert abs(own / (2 * eps) - dot(gx, step)) <= truncation + rounding
