@@ -849,8 +849,59 @@ __global__ void __launch_bounds__(kAttnWideThreads) k_attn_table(const __grid_co
   table_part(a, blockIdx.x);
 }
 
-// One warp per entry of gtable: the CTAs' partials in a fixed order, in 64 bits (a few hundred terms of
-// both signs).
+// Tables that leave a CTA few copies: one copy a CTA instead, whose buckets the lane groups share out (bucket b
+// belongs to group b mod G), so that an entry still has one thread, which adds its edges in order.  A tile of
+// edges is staged in shared memory; each warp looks through it 32 edges at a time, each group picks its own.
+// With the groups of table_part, 8,192 entries left one group of eight lanes to walk a CTA's 4,096 edges one
+// after another (46,080 edges, 8 heads, 1,024 buckets: 271 us of a backward pass of 310, now 23 of 62).  A CTA
+// has up to as many edges as there are buckets (256 at least, more from 296 CTAs on), and they may all be of one
+// bucket: chains of thousands of 32-bit additions, of values of both signs.
+constexpr int kTableThreads = 512, kTableTile = 256;
+
+__global__ void __launch_bounds__(kTableThreads) k_attn_large_table(const __grid_constant__ AttnArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  const int KH = a.K * a.H, lanes = a.hist_lanes;
+  float* const table = reinterpret_cast<float*>(dyn);
+  float* const ds = table + KH;                                    // [tile][H]
+  int* const keys = reinterpret_cast<int*>(ds + kTableTile * a.H); // [tile]: bucket, -1 for an edge that takes no part
+  let_next_launch();
+  for (int i = threadIdx.x; i < KH; i += kTableThreads) table[i] = 0.0f;
+  const int lo = max(0, min(__ldg(a.rowptr), a.E)), hi = max(lo, min(__ldg(a.rowptr + a.N), a.E));
+  const int first = lo + (int)((int64_t)(hi - lo) * blockIdx.x / a.hist_ctas);
+  const int last = lo + (int)((int64_t)(hi - lo) * (blockIdx.x + 1) / a.hist_ctas);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = 32 / lanes, groups = kTableThreads / lanes;
+  const int mine = lane / lanes, h = lane & (lanes - 1);
+  for (int e0 = first; e0 < last; e0 += kTableTile) {
+    const int n = min(kTableTile, last - e0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTableTile; i += kTableThreads) {
+      const int b = i < n && a.dst[e0 + i] >= 0 ? __ldg(a.bucket + e0 + i) : -1;
+      keys[i] = (unsigned)b < (unsigned)a.K ? b : -1;
+    }
+    for (int i = threadIdx.x; i < n * a.H; i += kTableThreads) ds[i] = a.rec[(int64_t)e0 * a.H + i].x;
+    __syncthreads();
+    for (int j = 0; j < n; j += 32) {
+      const int key = keys[j + lane], owner = key < 0 ? -1 : key & (groups - 1);
+      if (__ballot_sync(kFull, owner >= 0 && owner / per == warp) == 0) continue;
+      unsigned todo = 0;
+      for (int g = 0; g < per; ++g) {
+        const unsigned of_g = __ballot_sync(kFull, owner == warp * per + g);
+        if (g == mine) todo = of_g;
+      }
+      for (; todo != 0; todo &= todo - 1) {
+        const int i = j + __ffs(todo) - 1;
+        if (h < a.H) table[keys[i] * a.H + h] += ds[i * a.H + h];
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  float* const out = a.hist_ctas == 1 ? a.gtable : a.hist + (int64_t)blockIdx.x * KH;
+  for (int i = threadIdx.x; i < KH; i += kTableThreads) out[i] = table[i];
+}
+
+// One warp per entry of gtable: the CTAs' partials in a fixed order, in 64 bits (up to 1,184 terms of both
+// signs).
 __device__ __forceinline__ void table_sum(const AttnArgs& a, int o) {
   const int KH = a.K * a.H, lane = threadIdx.x & 31;
   if (o >= KH) return;
@@ -1220,25 +1271,41 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
-// Copies of the table per CTA: one per group of lanes while they fit 32 KB, at least one.  CTAs: enough that a
-// group has no more than some 48 edges, as long as a CTA has as many edges' values as it zeroes, sums
-// and writes floats.
-void hist_plan(AttnArgs& a, int threads) {
+// Small tables (table_part): copies per CTA, one per group of lanes while they fit 512 bytes a thread (256 from 2^20
+// edges on), 32 KB at most: behind the sender pass every CTA of that pass has this much shared memory too.  CTAs:
+// enough that a group has no more than some 48 edges, while they stay eight a SM and a CTA has as many edges'
+// values as it zeroes, sums and writes floats.  False where the latter leaves a group more than 128 edges, which
+// is where k_attn_large_table takes over.  Whole backward pass in us with the one and the other, 8 heads: 46,080
+// edges 64 buckets 42.5 / 49.3, 128 buckets 45.5 / 49.3, 192 58.6 / 51.2, 1,024 310 / 62; 3.0M edges 64 buckets
+// 1,472 / 1,598, 96 1,829 / 1,602, 256 2,564 / 1,602.  512 against 256 bytes a thread: 165,448 edges, 82 buckets
+// 733 / 741, 600,000 edges, 4 heads, 128 buckets 400 / 360, 3.0M edges, one head, 128 buckets 1,681 / 1,353.
+bool small_table_plan(AttnArgs& a, int threads) {
   a.hist_lanes = 1;
   while (a.hist_lanes < a.H) a.hist_lanes *= 2;
   const int KH = std::max(1, a.K * a.H);
-  a.hist_copies = std::max(1, std::min(threads / a.hist_lanes, 8 * 1024 / KH));
-  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(a.hist_copies * 48, KH / a.H * 4));
+  const int floats = std::min(8 * 1024, (a.E < 1 << 20 ? 128 : 64) * threads);
+  a.hist_copies = std::max(1, std::min(threads / a.hist_lanes, floats / KH));
+  const int64_t want = std::max<int64_t>(1, (int64_t)a.E / std::max(a.hist_copies * 48, 4 * a.K));
   a.hist_ctas = (int)std::min<int64_t>(want, 148 * 2 * (kAttnThreads / std::min(threads, kAttnThreads)));
+  return 4 * a.K <= 128 * a.hist_copies;
 }
 
-// Shared memory of a table_part CTA.
-size_t hist_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H * a.hist_copies; }
+// Large ones (k_attn_large_table): CTAs of at least a tile of edges and as many edges as buckets, two a SM.
+void large_table_plan(AttnArgs& a) {
+  a.hist_lanes = 1;
+  while (a.hist_lanes < a.H) a.hist_lanes *= 2;
+  a.hist_copies = 1;
+  a.hist_ctas = std::max(1, std::min(a.E / std::max(kTableTile, a.K), 148 * 2));
+}
 
-// The table's CTAs behind the sender pass's, with as many threads.
+// Shared memory of a CTA of the one and of the other.
+size_t small_table_bytes(const AttnArgs& a) { return sizeof(float) * (size_t)a.K * a.H * a.hist_copies; }
+size_t large_table_bytes(const AttnArgs& a) { return sizeof(float) * ((size_t)a.K * a.H + kTableTile * (a.H + 1)); }
+
+// Notes the threads of a pass's CTAs; a table behind the sender pass has CTAs of as many.
 void plan_table(AttnArgs& a, int threads) {
   a.threads = threads;
-  if (a.table_here) hist_plan(a, threads);
+  if (a.table_here) small_table_plan(a, threads);
 }
 
 template <int V, int SQ, int SV, bool LOOSE, bool WIDE>
@@ -1250,7 +1317,7 @@ cudaError_t launch_one(Pass pass, const AttnArgs& a, int threads, cudaStream_t s
   if (WIDE || a.W > 1) smem += sizeof(float) * join_floats(pass, V, SQ, SV, WIDE, rows_at_once(pass, V, SV, WIDE));
   const unsigned grid = (unsigned)(a.row_ctas + a.win_ctas);
   if (pass == kSend) {
-    if (a.hist_ctas > 0) smem = std::max(smem, hist_bytes(a));
+    if (a.hist_ctas > 0) smem = std::max(smem, small_table_bytes(a));
     cudaError_t e = allow(k_attn_bwd_send<V, SQ, SV, LOOSE, WIDE>, smem);
     if (e != cudaSuccess) return e;
     return launch_after(k_attn_bwd_send<V, SQ, SV, LOOSE, WIDE>, grid + (unsigned)a.hist_ctas, threads, smem, s, a);
@@ -1378,11 +1445,10 @@ BwdLayout bwd_layout(const tp_attn_s* h, int64_t N, int64_t E) {
   a.N = (int)N;
   a.E = (int)E;
   window_plan(a);
-  int hist_ctas = 0;         // whatever the threads of the sender pass will be
-  for (int threads : {32, kAttnThreads, kAttnWideThreads}) {
-    hist_plan(a, threads);
-    hist_ctas = std::max(hist_ctas, a.hist_ctas);
-  }
+  large_table_plan(a);
+  int hist_ctas = a.hist_ctas;
+  for (int threads : {32, kAttnThreads, 2 * kAttnThreads, kAttnWideThreads})       // whatever the passes will have
+    if (small_table_plan(a, threads)) hist_ctas = std::max(hist_ctas, a.hist_ctas);
   BwdLayout L;
   size_t off = 0;
   const size_t e = (size_t)std::max<int64_t>(E, 1);
@@ -1642,20 +1708,27 @@ tp_status_t tp_attn_bwd(tp_attn_t attn, int64_t N, int64_t E, const int32_t* row
   tail.send_len = part_len(a, kSend);
   tail.recv_joins = gq ? join_ctas(a, a.dq) : 0;
   tail.send_joins = send ? join_ctas(a, a.dq + a.dv) : 0;
-  // behind the sender pass while a copy of the table leaves that pass's CTAs their shared memory
-  a.table_here = gtable && E > 0 && send && (size_t)a.K * a.H * sizeof(float) <= 32 * 1024;
+  a.table_here = 0;
   a.hist_ctas = 0;
   e = launch_pass(kRecv, a, width, tail.recv_part, s);
+  // a small table's CTAs come behind the sender pass's where there is one; its plan is the same without
+  const bool table_wanted = gtable && E > 0, small = table_wanted && small_table_plan(a, a.threads);
+  a.table_here = small && send;
   a.hist_ctas = 0;
   if (e == cudaSuccess && send) e = launch_pass(kSend, a, width, tail.send_part, s);
-  if (e == cudaSuccess && gtable && E > 0 && !a.table_here) {
-    hist_plan(a, a.threads);
-    const size_t smem = hist_bytes(a);
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_attn_table, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && table_wanted && !a.table_here) {
     // an ordinary launch: set up early, its few CTAs would gather on the SMs that the receiver pass leaves
     // first and run there one after another (162,892 edges: 46 instead of 16 us)
+    if (small) {
+      small_table_plan(a, a.threads);
+      k_attn_table<<<a.hist_ctas, a.threads, small_table_bytes(a), s>>>(a);
+    } else {
+      large_table_plan(a);
+      const size_t smem = large_table_bytes(a);
+      if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_attn_large_table, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e == cudaSuccess) k_attn_large_table<<<a.hist_ctas, kTableThreads, smem, s>>>(a);
+    }
     if (e == cudaSuccess) {
-      k_attn_table<<<a.hist_ctas, a.threads, smem, s>>>(a);
       count_launches(1);
       e = cudaGetLastError();
     }
