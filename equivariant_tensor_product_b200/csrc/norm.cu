@@ -16,8 +16,9 @@
 // 18,262 rows of five blocks of 78 channels went from 78 to 47 us forward and 213 to 102 backward against
 // single floats.
 //
-// Blocks of more than 1,152 floats take one CTA per row with three reads of the row, the later ones
-// from L1: k_norm_any.
+// Blocks of more than 1,152 floats (36 a lane) take one CTA per row, all blocks of it, with three reads of the
+// row, the later ones from L1: k_norm_any.  100,000 rows: 228x2e 147 us forward and 239 backward in registers,
+// 256x2e 209 and 903 there.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -161,7 +162,9 @@ struct RowLanes {
 
 // Rows in flight a group: up to 16 floats a lane on their way, 8 with single floats, whose addresses and
 // limits take as many registers as their data (311,042 rows of 21 channels, four blocks, backward: 579 us
-// with 8 floats in flight, 622 with 16, which spill).
+// with 8 floats in flight, 622 with 16).  At the registers that ctas_per_sm leaves the backward kernel spills
+// some words in the 16- and 8-byte forms too: 60 bytes read back a thread with 16-byte chunks and one a lane, 152
+// with 8-byte chunks and up to two.
 __host__ __device__ constexpr int rows_in_flight(int V, int S) {
   return V == 4 ? (S == 1 ? 4 : S == 2 ? 2 : 1) : S <= 2 ? 4 : S <= 4 ? 2 : 1;
 }
