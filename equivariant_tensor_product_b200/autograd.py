@@ -10,23 +10,41 @@ from __future__ import annotations
 import torch
 
 from ._lib import TP_MODE_UVW
+from ._marshal import stream_of
 from .ops import (Plan, tp_conv_bwd, tp_conv_bwd_radial, tp_conv_dbwd, tp_conv_fwd, tp_conv_fwd_radial,
                   tp_csr_transpose)
 
 
+def _capturing():
+    return torch.cuda.is_current_stream_capturing()
+
+
 class Graph:
-    """Receiver-sorted CSR plus a lazily built stable sender transpose (int32, on device)."""
+    """Receiver-sorted CSR plus a lazily built stable sender transpose (int32, on device).  The transpose is kept from
+    the first call that needs it on; calls on other streams wait for the stream that built it."""
 
     def __init__(self, rowptr: torch.Tensor, src: torch.Tensor):
         self.rowptr = rowptr.to(torch.int32).contiguous()
         self.src = src.to(torch.int32).contiguous()
         self.N = self.rowptr.numel() - 1
+        self._device = self.rowptr.get_device()
         self._colptr = None
         self._perm = None
+        self._built = None                   # (raw stream, event behind the transpose on it)
 
     def transpose(self):
         if self._colptr is None:
-            self._colptr, self._perm = tp_csr_transpose(self.rowptr, self.src, self.N)
+            colptr, perm = tp_csr_transpose(self.rowptr, self.src, self.N)
+            if _capturing():
+                return colptr, perm          # exists from the first replay on: the captured call's alone
+            self._built = stream_of(self._device), torch.cuda.current_stream(self._device).record_event()
+            self._perm = perm
+            self._colptr = colptr            # last: what another thread looks at
+        elif stream_of(self._device) != self._built[0] and not _capturing():
+            stream = torch.cuda.current_stream(self._device)     # torch.cuda.graph synchronises before a capture
+            stream.wait_event(self._built[1])
+            self._colptr.record_stream(stream)
+            self._perm.record_stream(stream)
         return self._colptr, self._perm
 
 

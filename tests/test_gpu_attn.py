@@ -492,3 +492,25 @@ def test_outputs_in_place_of_inputs_are_refused(tp):
         with pytest.raises(ValueError, match="share memory"):
             tp.tp_attn_bwd(attn, *rows, y, lse, g["gy"], **given, **more)
     tp.tp_attn_bwd(attn, *rows, y, lse, g["gy"], gq=own, **more)
+
+
+def test_a_sender_order_first_made_on_another_stream(tp):
+    """A backward call on one stream while the order that it shares is still being built on another."""
+    pr = problem(41, "8x0e+4x1o", "8x0e+4x1o", 4, n=400, mean_degree=20)
+    want = solve(tp, pr)
+    d = {k: dev(a) for k, a in pr["d"].items()}
+    attn, graph = tp.Attention(pr["qk"], pr["v"], pr["heads"], pr["n_buckets"]), tp.autograd.Graph(d["rowptr"], d["src"])
+    q, k, v = (d[name].requires_grad_(True) for name in ("q", "k", "v"))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            y = tp.tp_attn(attn, graph, q, k, v, d["bucket"], d["table"], pr["scale"])
+            if i == 0:
+                torch.cuda._sleep(50_000_000)                  # some 25 ms before the order is built
+            got.append(torch.autograd.grad(y, (q, k, v), d["gy"]))
+    torch.cuda.synchronize()
+    for grads in got:
+        for g, name in zip(grads, ("gq", "gk", "gv")):
+            assert torch.equal(g, want[name]), name
